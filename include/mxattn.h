@@ -273,6 +273,96 @@ mxattn_status mxattn_forward_noalloc(const void* q, const void* k, const void* v
                                      void* stream);
 
 /*
+ * Paged MXFP4 KV cache: keys and values that stay in MXFP4 between calls, and attention of new
+ * tokens over them (decoding, chunked prefill, cross attention to cached states).
+ *
+ * The cache is a pool of n_pages pages of page_size tokens (a power of two from 16 to 256) for
+ * Hkv heads of d in {64, 128} channels: device memory of n_pages * mxattn_cache_page_bytes(...)
+ * bytes, 16-byte aligned, [n_pages][Hkv][K, V][page_size * 17 d / 32]. A chunk holds page_size
+ * rows of d/2 code bytes and then page_size rows of d/32 scale bytes, blocks of 32 along d for
+ * both K and V (a token is added without touching its neighbours), the bytes interleaved for the
+ * attention kernels (csrc/cache_layout.cuh): written by mxattn_cache_append, read back as values
+ * by mxattn_cache_read. Slot s is token s % page_size of page s / page_size.
+ * Lengths, tables and slots live on the device: a call sees their values when it runs, so the same
+ * calls can be captured into a CUDA graph and replayed for changing batches (host arguments are
+ * upper bounds). Values on the device that would lead out of a buffer are not followed: each call
+ * says below what it does with them.
+ */
+
+/* Bytes of one page; 0 for unsupported shapes. */
+size_t mxattn_cache_page_bytes(int Hkv, int page_size, int d);
+
+/*
+ * mxattn_cache_plan -- block tables and slot maps of a batch, from its requests' lengths.
+ *   ctx_len, new_len : int32 [R], tokens that request r has in the cache, and tokens it adds now
+ *   block_table      : int32 [R, table_width], in and out: row r starts with the pages of its
+ *                      ceil(ctx_len / page_size) held pages; the entries of the pages it needs for
+ *                      the new tokens are written, all others are left as they were
+ *   free_pages       : int32 [n_free], handed out from the front in the order of the requests
+ * Outputs:
+ *   q_start : int32 [R + 1], first row of each request's new tokens, and their number
+ *   kv_len  : int32 [R], ctx_len + new_len
+ *   slots   : int64 [max_tokens], slot of each new token; -1 for rows behind the last request
+ *   info    : int32 [4]: new tokens, pages taken from the front of free_pages, requests refused, 0
+ * A request is refused when a length is negative, its rows would pass max_tokens, its pages
+ * table_width, or the free pages are used up: its table row stays as it was, its tokens get slot -1
+ * and its kv_len is ctx_len (0 if that is negative). A refused request takes no page, except that
+ * once the free pages have run out every later request that needs one is refused too. The rows of
+ * refused requests count in q_start, up to max_tokens. One launch; max_tokens < 2^31.
+ */
+mxattn_status mxattn_cache_plan(const int32_t* ctx_len, const int32_t* new_len, int R, int32_t* block_table,
+                                int table_width, const int32_t* free_pages, int n_free, int page_size,
+                                int32_t* q_start, int32_t* kv_len, int64_t* slots, int64_t max_tokens, int32_t* info,
+                                void* stream);
+
+/*
+ * mxattn_cache_append -- quantize the K and V rows of T tokens into their slots.
+ *   k, v  : bf16, element (t, h, c) at t * token_stride + h * head_stride + c (strides in elements,
+ *           not negative: rows of a fused QKV projection can be passed as they are); 2-byte
+ *           aligned, 16-byte aligned rows enable vector loads
+ *   slots : int64 [T]; tokens whose slot is outside [0, n_pages * page_size) are skipped. The slots
+ *           of one call differ: a slot that is given twice ends up with parts of both tokens.
+ *   scale_mode: MXATTN_SCALE_OCP or MXATTN_SCALE_UOS. Codes and scales are those of mxattn_quantize
+ *           (transpose = 0) on the rows; finite inputs, as there. One launch.
+ * mxattn_cache_read -- the values of T slots as bf16 k, v [T, Hkv, d] (contiguous, 16-byte aligned):
+ *   code times scale, exactly (a value above the bf16 range becomes infinite, one below it is
+ *   rounded). Rows whose slot is outside the cache are zero. One launch.
+ */
+mxattn_status mxattn_cache_append(const void* k, int64_t k_token_stride, int64_t k_head_stride, const void* v,
+                                  int64_t v_token_stride, int64_t v_head_stride, const int64_t* slots, int64_t T,
+                                  int Hkv, int d, int page_size, int64_t n_pages, int scale_mode, uint8_t* cache,
+                                  void* stream);
+mxattn_status mxattn_cache_read(const uint8_t* cache, const int64_t* slots, int64_t T, int Hkv, int d, int page_size,
+                                int64_t n_pages, void* k, void* v, void* stream);
+
+/*
+ * mxattn_paged_forward -- attention of the new tokens of R requests over their pages.
+ *   q       : bf16, element (t, h, c) at t * q_token_stride + h * q_head_stride + c; 16-byte
+ *             aligned, strides multiples of 8 elements. Rows q_start[r] .. q_start[r + 1] - 1 are
+ *             request r's n new tokens; query head h reads KV head h / (Hq / Hkv).
+ *   out     : bf16 [T, Hq, d] contiguous, 16-byte aligned
+ *   lse     : fp32 [T, Hq] or NULL: natural log of the sum of exp(score) (-infinity for no key)
+ *   out_i = sum_j softmax_j(q_i . k_j / sqrt(d)) v_j, with the cache's values of k and v. Token i of
+ *   n attends to keys j <= kv_len - n + i (causal = 1), or to all j < kv_len (causal = 0: cross
+ *   attention to cached states of any other length). Scores and sums are fp32, Q is not quantized,
+ *   the probabilities enter their product with 8 significant bits or more.
+ *   A row with no key gets out = 0. Rows of no request are left as they were.
+ *   max_new, max_kv: upper bounds of the requests' new tokens and of kv_len, from which the work is
+ *   laid out; rows of a request past max_new are left as they were, keys past max_kv or past
+ *   table_width pages are not attended to. Table entries outside [0, n_pages) count as no keys.
+ *   q_start values are clamped to [0, T], a negative kv_len counts as 0.
+ *   workspace: mxattn_paged_workspace_size(...) bytes, 256-byte aligned, contents on entry ignored,
+ *   not used concurrently by another call; its first word is the status word of
+ *   mxattn_check_status. A call with T, R or max_new 0 does nothing and leaves it as it was.
+ */
+size_t mxattn_paged_workspace_size(int64_t T, int R, int Hq, int Hkv, int d, int max_new, int64_t max_kv);
+mxattn_status mxattn_paged_forward(const void* q, int64_t q_token_stride, int64_t q_head_stride, const uint8_t* cache,
+                                   const int32_t* block_table, int table_width, const int32_t* q_start,
+                                   const int32_t* kv_len, void* out, float* lse, int64_t T, int R, int Hq, int Hkv,
+                                   int d, int page_size, int64_t n_pages, int max_new, int64_t max_kv, int causal,
+                                   void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * mxattn_check_status -- synchronises `stream`, reads and clears the workspace status word.
  * Returns MXATTN_ERR_TIMEOUT if a kernel gave up on a bounded wait since the last check (the
  * raw code goes to *detail when detail != NULL), MXATTN_ERR_CUDA on a CUDA error, else MXATTN_OK.

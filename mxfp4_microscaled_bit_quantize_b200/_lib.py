@@ -33,6 +33,15 @@ SIGNATURES = {
     "mxattn_quantize_nvfp4": (_c_int, [_vp, _c_i64, _c_i64, _u8p, _u8p, _vp]),
     "mxattn_gemm_nvfp4_workspace_size": (_c_size, [_c_i64] * 3),
     "mxattn_gemm_nvfp4": (_c_int, [_u8p] * 4 + [_vp] + [_c_i64] * 3 + [_c_int, _vp, _c_size, _vp]),
+    "mxattn_cache_page_bytes": (_c_size, [_c_int] * 3),
+    "mxattn_cache_plan": (_c_int, [_vp, _vp, _c_int, _vp, _c_int, _vp, _c_int, _c_int, _vp, _vp, _vp, _c_i64, _vp,
+                                   _vp]),
+    "mxattn_cache_append": (_c_int, [_vp, _c_i64, _c_i64, _vp, _c_i64, _c_i64, _vp, _c_i64] + [_c_int] * 3
+                            + [_c_i64, _c_int, _u8p, _vp]),
+    "mxattn_cache_read": (_c_int, [_u8p, _vp, _c_i64] + [_c_int] * 3 + [_c_i64, _vp, _vp, _vp]),
+    "mxattn_paged_workspace_size": (_c_size, [_c_i64] + [_c_int] * 5 + [_c_i64]),
+    "mxattn_paged_forward": (_c_int, [_vp, _c_i64, _c_i64, _u8p, _vp, _c_int, _vp, _vp, _vp, _vp, _c_i64]
+                             + [_c_int] * 5 + [_c_i64, _c_int, _c_i64, _c_int, _vp, _c_size, _vp]),
     "mxattn_check_status": (_c_int, [_vp, _vp, ctypes.POINTER(ctypes.c_uint)]),
     "mxattn_check_status_noalloc": (_c_int, [_vp, ctypes.POINTER(ctypes.c_uint)]),
     "mxattn_status_string": (ctypes.c_char_p, [_c_int]),

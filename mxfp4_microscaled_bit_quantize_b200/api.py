@@ -286,6 +286,174 @@ def mxattn_forward_debug(q, k, v, dbg_bh: int, r0: int, r1: int, causal: bool = 
     return out, pc, ps
 
 
+def cache_alloc(n_pages: int, Hkv: int, d: int, page_size: int = 16, device="cuda") -> torch.Tensor:
+    """An empty paged MXFP4 KV cache: uint8 [n_pages, Hkv, 2 (K, V), page_size, 17 d / 32]. d in {64, 128},
+    page_size a power of two from 16 to 256."""
+    if _lib.load().mxattn_cache_page_bytes(Hkv, page_size, d) == 0:
+        raise ValueError("unsupported cache shape (d in {64, 128}, page_size a power of two from 16 to 256)")
+    return torch.zeros((n_pages, Hkv, 2, page_size, 17 * d // 32), dtype=torch.uint8, device=device)
+
+
+def _cache(cache):
+    """(n_pages, Hkv, page_size, d) of a cache tensor."""
+    _need(cache, "cache", torch.uint8)
+    if cache.dim() != 5 or cache.shape[2] != 2 or cache.shape[4] % 17 != 0:
+        raise ValueError("cache must be [n_pages, Hkv, 2, page_size, 17 d / 32]")
+    n_pages, Hkv, _, P, row = cache.shape
+    return n_pages, Hkv, P, row // 17 * 32
+
+
+def _on(dev, **tensors) -> None:
+    for name, t in tensors.items():
+        if t.device != dev:
+            raise ValueError(f"{name} must be on {dev}, got {t.device}")
+
+
+def mxattn_cache_plan(ctx_len, new_len, block_table, free_pages, page_size: int, max_tokens: int, out=None):
+    """Block tables and slot maps of a batch from its requests' lengths.
+
+    ctx_len, new_len [R], block_table [R, width] (the pages each request holds; new ones are written in place),
+    free_pages [F]: int32 CUDA tensors. Returns (q_start [R + 1] int32, kv_len [R] int32, slots [max_tokens] int64,
+    info [4] int32: new tokens, free pages taken, requests refused, 0); `out` takes the same four to be written in
+    place. A request that does not fit (rows past max_tokens, pages past the table or the free list) is refused:
+    its slots are -1, as are those behind the last request."""
+    for t, n in ((ctx_len, "ctx_len"), (new_len, "new_len"), (block_table, "block_table"), (free_pages, "free_pages")):
+        _need(t, n, torch.int32)
+    dev = ctx_len.device
+    R = ctx_len.numel()
+    if ctx_len.dim() != 1 or new_len.shape != ctx_len.shape or block_table.dim() != 2 or block_table.shape[0] != R:
+        raise ValueError("ctx_len, new_len must be [R] and block_table [R, width]")
+    if free_pages.dim() != 1 or max_tokens < 0:
+        raise ValueError("free_pages must be [F] and max_tokens not negative")
+    _on(dev, new_len=new_len, block_table=block_table, free_pages=free_pages)
+    if out is None:
+        ints = torch.empty(2 * R + 5, dtype=torch.int32, device=dev)
+        q_start, kv_len, info = ints[:R + 1], ints[R + 1:2 * R + 1], ints[2 * R + 1:]
+        slots = torch.empty(max_tokens, dtype=torch.int64, device=dev)
+    else:
+        q_start, kv_len, slots, info = out
+        for t, shape, dt, n in ((q_start, (R + 1,), torch.int32, "q_start"), (kv_len, (R,), torch.int32, "kv_len"),
+                                (slots, (max_tokens,), torch.int64, "slots"), (info, (4,), torch.int32, "info")):
+            _need(t, n, dt)
+            if tuple(t.shape) != shape:
+                raise ValueError(f"{n} must have shape {shape}, got {tuple(t.shape)}")
+            _on(dev, **{n: t})
+    with torch.cuda.device(dev):
+        st = _lib.load().mxattn_cache_plan(ctx_len.data_ptr(), new_len.data_ptr(), R, block_table.data_ptr(),
+                                           block_table.shape[1], free_pages.data_ptr(), free_pages.numel(), page_size,
+                                           q_start.data_ptr(), kv_len.data_ptr(), slots.data_ptr(), max_tokens,
+                                           info.data_ptr(), _stream(dev))
+    _lib.check(st, "mxattn_cache_plan")
+    return q_start, kv_len, slots, info
+
+
+def _rows(t, name, H, d):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.dim() != 3 or (H is not None and t.shape[1] != H) or t.shape[2] != d or t.stride(2) != 1:
+        raise ValueError(f"{name} must be [T, heads, {d}] with contiguous rows, got {tuple(t.shape)}")
+
+
+def mxattn_cache_append(k, v, slots, cache, scale_mode: int = SCALE_UOS) -> None:
+    """Quantize k, v [T, Hkv, d] (bf16, rows contiguous, any token and head strides) into the cache's slots
+    (int64 [T]; a slot outside the cache skips its token; slots of one call must differ)."""
+    n_pages, Hkv, P, d = _cache(cache)
+    _need(slots, "slots", torch.int64)
+    _rows(k, "k", Hkv, d)
+    _rows(v, "v", Hkv, d)
+    T = k.shape[0]
+    if v.shape[0] != T or slots.dim() != 1 or slots.shape[0] != T:
+        raise ValueError("k, v and slots must have the same number of tokens")
+    dev = cache.device
+    _on(dev, k=k, v=v, slots=slots)
+    with torch.cuda.device(dev):
+        st = _lib.load().mxattn_cache_append(k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0),
+                                             v.stride(1), slots.data_ptr(), T, Hkv, d, P, n_pages, int(scale_mode),
+                                             cache.data_ptr(), _stream(dev))
+    _lib.check(st, "mxattn_cache_append")
+
+
+def mxattn_cache_read(cache, slots, out=None):
+    """(k, v) [T, Hkv, d] bf16: the values that the slots (int64 [T]) hold; zeros for slots outside the cache."""
+    n_pages, Hkv, P, d = _cache(cache)
+    _need(slots, "slots", torch.int64)
+    if slots.dim() != 1:
+        raise ValueError("slots must be [T]")
+    T, dev = slots.shape[0], cache.device
+    _on(dev, slots=slots)
+    if out is None:
+        k, v = torch.empty((2, T, Hkv, d), dtype=torch.bfloat16, device=dev).unbind(0)
+    else:
+        k, v = out
+        for t, n in ((k, "k"), (v, "v")):
+            _need(t, n)
+            if tuple(t.shape) != (T, Hkv, d):
+                raise ValueError(f"{n} must have shape {(T, Hkv, d)}, got {tuple(t.shape)}")
+        _on(dev, k=k, v=v)
+    with torch.cuda.device(dev):
+        st = _lib.load().mxattn_cache_read(cache.data_ptr(), slots.data_ptr(), T, Hkv, d, P, n_pages, k.data_ptr(),
+                                           v.data_ptr(), _stream(dev))
+    _lib.check(st, "mxattn_cache_read")
+    return k, v
+
+
+def paged_workspace_size(T: int, R: int, Hq: int, Hkv: int, d: int, max_new: int, max_kv: int) -> int:
+    return int(_lib.load().mxattn_paged_workspace_size(T, R, Hq, Hkv, d, max_new, max_kv))
+
+
+def mxattn_paged_forward(q, cache, block_table, q_start, kv_len, max_new: int, max_kv: int | None = None,
+                         causal: bool = True, workspace: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                         lse: torch.Tensor | None = None) -> torch.Tensor:
+    """Attention of the new tokens q [T, Hq, d] (bf16, rows contiguous) of R requests over the paged MXFP4 cache.
+
+    block_table [R, width], q_start [R + 1], kv_len [R] (int32, as mxattn_cache_plan makes them); max_new, max_kv:
+    upper bounds of a request's new tokens and of kv_len (default: what the table holds). causal: token i of n sees
+    keys up to kv_len - n + i; otherwise all kv_len (cross attention). Returns out [T, Hq, d] bf16; rows of no
+    request are left as they were (whatever they held, in a new `out`). lse: optional fp32 [T, Hq] to be written."""
+    n_pages, Hkv, P, d = _cache(cache)
+    _rows(q, "q", None, d)
+    for t, n in ((block_table, "block_table"), (q_start, "q_start"), (kv_len, "kv_len")):
+        _need(t, n, torch.int32)
+    T, Hq = q.shape[0], q.shape[1]
+    R, dev = kv_len.numel(), cache.device
+    if block_table.dim() != 2 or block_table.shape[0] != R or kv_len.dim() != 1 or tuple(q_start.shape) != (R + 1,):
+        raise ValueError("block_table must be [R, width], q_start [R + 1] and kv_len [R]")
+    _on(dev, q=q, block_table=block_table, q_start=q_start, kv_len=kv_len)
+    width = block_table.shape[1]
+    if max_kv is None:
+        max_kv = width * P
+    if out is None:
+        out = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=dev)
+    else:
+        _need(out, "out")
+        if tuple(out.shape) != (T, Hq, d):
+            raise ValueError(f"out must have shape {(T, Hq, d)}, got {tuple(out.shape)}")
+        _on(dev, out=out)
+    if lse is not None:
+        _need(lse, "lse", torch.float32)
+        if tuple(lse.shape) != (T, Hq):
+            raise ValueError(f"lse must have shape {(T, Hq)}, got {tuple(lse.shape)}")
+        _on(dev, lse=lse)
+    lib = _lib.load()
+    if workspace is None:
+        n = int(lib.mxattn_paged_workspace_size(T, R, Hq, Hkv, d, max_new, max_kv))
+        if n == 0:
+            raise ValueError("unsupported attention shape")
+        workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+    else:
+        _need(workspace, "workspace", torch.uint8)
+        _on(dev, workspace=workspace)
+    with torch.cuda.device(dev):
+        st = lib.mxattn_paged_forward(q.data_ptr(), q.stride(0), q.stride(1), cache.data_ptr(), block_table.data_ptr(),
+                                      width, q_start.data_ptr(), kv_len.data_ptr(), out.data_ptr(),
+                                      None if lse is None else lse.data_ptr(), T, R, Hq, Hkv, d, P, n_pages, max_new,
+                                      max_kv, int(bool(causal)), workspace.data_ptr(), workspace.numel(), _stream(dev))
+    _lib.check(st, "mxattn_paged_forward")
+    return out
+
+
 def mxattn_check_status(workspace: torch.Tensor) -> int:
     """Synchronises the current stream; returns the device status word (0 = ok)."""
     detail = ctypes.c_uint(0)

@@ -129,6 +129,60 @@ struct GemmParams {
 cudaError_t launch_gemm(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap& tmC, const GemmParams& p,
                         cudaStream_t stream);
 
+// Paged MXFP4 KV cache (layout: cache_layout.cuh). Pages of 1 << page_shift tokens.
+struct PlanParams {
+  const int32_t* ctx_len;   // [R]
+  const int32_t* new_len;   // [R]
+  int R;
+  int32_t* block_table;     // [R, table_width]
+  int table_width;
+  const int32_t* free_pages;
+  int n_free;
+  int page_shift;
+  int32_t* q_start;         // [R + 1]
+  int32_t* kv_len;          // [R]
+  int64_t* slots;           // [max_tokens]
+  int64_t max_tokens;
+  int32_t* info;            // [4]
+};
+cudaError_t launch_plan(const PlanParams& p, cudaStream_t stream);
+
+struct AppendParams {
+  const __nv_bfloat16 *k, *v;
+  int64_t k_token_stride, k_head_stride, v_token_stride, v_head_stride;   // elements
+  const int64_t* slots;     // [T]
+  int64_t T, n_slots;       // n_slots = pages << page_shift
+  int Hkv, page_shift, mode;
+  int k_vec, v_vec;         // 16-byte loads allowed
+  uint8_t* cache;
+};
+cudaError_t launch_append(const AppendParams& p, int d, cudaStream_t stream);
+
+struct ReadParams {
+  const uint8_t* cache;
+  const int64_t* slots;     // [T]
+  int64_t T, n_slots;
+  int Hkv, page_shift;
+  __nv_bfloat16 *k, *v;     // [T, Hkv, d]
+};
+cudaError_t launch_read(const ReadParams& p, int d, cudaStream_t stream);
+
+struct PagedParams {
+  const __nv_bfloat16* q;
+  int64_t q_token_stride, q_head_stride;   // elements
+  const uint8_t* cache;
+  const int32_t* block_table;              // [R, table_width]
+  const int32_t* q_start;                  // [R + 1]
+  const int32_t* kv_len;                   // [R]
+  __nv_bfloat16* out;                      // [T, Hq, d]
+  float* lse;                              // [T, Hq] or null
+  int64_t T, n_pages, max_kv;
+  int R, Hq, Hkv, table_width, page_shift, max_new, causal;
+  float scale_log2;                        // log2(e) / sqrt(d)
+  unsigned int* status;                    // device status word (0 = ok), cleared by every call
+};
+cudaError_t launch_paged(const PagedParams& p, int d, cudaStream_t stream);
+
 // Status codes written by kernels into the workspace status word.
 enum : unsigned int {
   kStatusTimeoutQ = 0x100,
