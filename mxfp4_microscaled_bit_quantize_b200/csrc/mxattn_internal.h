@@ -181,7 +181,20 @@ struct PagedParams {
   float scale_log2;                        // log2(e) / sqrt(d)
   unsigned int* status;                    // device status word (0 = ok), cleared by every call
 };
-cudaError_t launch_paged(const PagedParams& p, int d, cudaStream_t stream);
+// How the work of a call is laid out, from the host's bounds alone.
+struct SplitPlan {
+  int nt;                  // 8-column tiles of query rows per CTA
+  int64_t row_tiles, chunk, splits, units;
+  int64_t part_rows;       // partial rows in the workspace (0: one split)
+};
+SplitPlan plan_splits(int64_t T, int R, int Hq, int Hkv, int d, int max_new, int64_t max_kv);
+struct SplitParams {
+  int64_t chunk;           // keys of one split
+  uint32_t splits, row_tiles;
+  float* part_o;           // [T, Hq, splits, d] normalised partial rows
+  float* part_lse;         // [T, Hq, splits] log2 of their sums
+};
+cudaError_t launch_paged(const PagedParams& p, const SplitPlan& s, void* part, int d, cudaStream_t stream);
 
 // Status codes written by kernels into the workspace status word.
 enum : unsigned int {

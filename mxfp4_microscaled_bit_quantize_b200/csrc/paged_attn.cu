@@ -1,5 +1,27 @@
-// Attention of new tokens over the paged MXFP4 KV cache: the simplest form, one warp per (token,
-// query head), one key at a time, all arithmetic in fp32.
+// Attention of few new tokens over the paged MXFP4 KV cache (decoding, drafted tokens to verify).
+//
+//   x_j = (q . k_j) log2(e) / sqrt(d),  out = sum_j 2^(x_j - m) v_j / sum_j 2^(x_j - m)
+//
+// Bound: 17/16 d bytes of K and V per key and KV head have to come from HBM once, for all query heads
+// of the group and all new tokens; at 6.5 TB/s an SM may spend about 90 clocks on 16 keys of d = 128.
+// So the kernel keeps the instructions per key down rather than the FLOPs:
+//   * a warp takes 16 keys at a time straight from global memory into mma fragments (the cache's
+//     layout does the gather, see cache_layout.cuh), one group ahead of the one it works on; the
+//     four warps of a CTA take turns on the groups and meet once, at the end;
+//   * S^T = K Q^T and O^T += V^T P^T with mma.m16n8k16: the keys (or channels) are the 16 rows, the
+//     queries (tokens x heads of the group) the 8 columns, so that decoding wastes no half tile;
+//   * E2M1 codes become fp16 by cvt (exact, 64 codes pairs per clock and SM); no scale is ever
+//     multiplied into K or V: a K block's scale multiplies its 32-channel partial score in fp32, a V
+//     block's scale its fp16 probability, four multiplications each for 8 queries instead of 16;
+//   * Q is fp16 after a power of two per row that brings its largest element to [2^7, 2^8) (bf16's 8
+//     bits fit, elements 2^-21 below the largest and smaller lose bits below 2^-32 of it);
+//   * the reference m of a column moves only when a score passes it by 7, so that the maximum over
+//     the warp's lanes is rarely taken; p = 2^(x - m + 7) <= 2^14 is summed in fp32 and rounded to
+//     fp16 (11 bits) for the product;
+//   * V's block scales enter relative to r_b, the largest exponent so far of channel block b, as
+//     2^(s - r_b) in fp16. A group with a block more than 14 binades below r_b takes a slower path
+//     with bf16 operands, whose range needs no such care.
+// A long context is split over CTAs (chunk keys each); their results meet in combine_kernel.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cmath>
@@ -11,77 +33,588 @@
 
 namespace mxattn {
 
-// Value of channel c of a row (K: which = 0).
-template <int D>
-__device__ __forceinline__ float cache_value(const uint8_t* chunk, uint32_t off, uint32_t c, int which, int page_shift) {
-  constexpr uint32_t NB = D / 32;
-  const uint32_t b = c >> 5, e = c & 31u;
-  const uint32_t byte = which == 0 ? (e >> 3) * (4 * NB) + 4 * b + ((e & 7u) >> 1)
-                                   : (e >> 2) * (2 * NB) + 2 * b + ((e & 3u) >> 1);
-  const uint32_t raw = chunk[off * (D / 2) + byte];
-  const uint32_t code = (c & 1u) ? raw >> 4 : raw & 15u;
-  const uint32_t i = off & 15u;
-  const uint32_t srow = off - i + (which ? v_scale_row(i) : k_scale_row(i));
-  const uint32_t s = chunk[((D / 2u) << page_shift) + srow * NB + b];
-  uint32_t h[4];
-  e2m1x8_to_half2(code, h);
-  return __half2float(__low2half(*reinterpret_cast<const __half2*>(&h[0]))) * pow2_from_byte(s);
+constexpr int kSmallWarps = 4;
+
+template <int NB> struct Frag;          // what a lane holds of 16 keys
+template <> struct Frag<4> { uint4 k0, k1; uint2 ks; uint2 v[4]; uint4 vs; };
+template <> struct Frag<2> { uint2 k0, k1; uint32_t ks; uint32_t v[4]; uint2 vs; };
+
+__device__ __forceinline__ uint4 ldg16(const uint8_t* p) {
+  uint4 r;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+  return r;
+}
+__device__ __forceinline__ uint2 ldg8(const uint8_t* p) {
+  uint2 r;
+  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
+  return r;
+}
+__device__ __forceinline__ uint32_t ldg4(const uint8_t* p) {
+  uint32_t r;
+  asm volatile("ld.global.nc.L1::no_allocate.u32 %0, [%1];" : "=r"(r) : "l"(p));
+  return r;
 }
 
-template <int D>
-__global__ void __launch_bounds__(128) paged_simple_kernel(const PagedParams p) {
-  constexpr int C = D / 32;
-  const int lane = threadIdx.x & 31;
+// kc: the page's K chunk of this head; off: first of the 16 tokens in the page.
+__device__ __forceinline__ void load_frag(Frag<4>& f, const uint8_t* kc, uint32_t off, int page_shift, uint32_t lane) {
+  const uint32_t g = lane >> 2, c = lane & 3u;
+  const uint8_t* k = kc + off * 64u + lane * 16u;
+  f.k0 = ldg16(k);
+  f.k1 = ldg16(k + 512);
+  const uint32_t codes = 64u << page_shift;
+  f.ks = ldg8(kc + codes + off * 4u + g * 8u);
+  const uint8_t* vc = kc + codes + (4u << page_shift);
+  const uint8_t* v = vc + (off + 2u * c) * 64u + g * 8u;
+  f.v[0] = ldg8(v);
+  f.v[1] = ldg8(v + 64);
+  f.v[2] = ldg8(v + 512);
+  f.v[3] = ldg8(v + 576);
+  f.vs = ldg16(vc + codes + off * 4u + c * 16u);
+}
+__device__ __forceinline__ void load_frag(Frag<2>& f, const uint8_t* kc, uint32_t off, int page_shift, uint32_t lane) {
+  const uint32_t g = lane >> 2, c = lane & 3u;
+  const uint8_t* k = kc + off * 32u + lane * 8u;
+  f.k0 = ldg8(k);
+  f.k1 = ldg8(k + 256);
+  const uint32_t codes = 32u << page_shift;
+  f.ks = ldg4(kc + codes + off * 2u + g * 4u);
+  const uint8_t* vc = kc + codes + (2u << page_shift);
+  const uint8_t* v = vc + (off + 2u * c) * 32u + g * 4u;
+  f.v[0] = ldg4(v);
+  f.v[1] = ldg4(v + 32);
+  f.v[2] = ldg4(v + 256);
+  f.v[3] = ldg4(v + 288);
+  f.vs = ldg8(vc + codes + off * 2u + c * 8u);
+}
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+               : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_bf162(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t word_of(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+__device__ __forceinline__ uint32_t word_of(const uint2& v, int i) { return i == 0 ? v.x : v.y; }
+__device__ __forceinline__ uint32_t word_of(uint32_t v, int) { return v; }
+
+// Scale bytes of block b for the lane's keys g and g + 8 as fp32 powers of two (byte 0 becomes 0).
+__device__ __forceinline__ float pow2_bits(uint32_t w, int b) {
+  const uint32_t x = b < 3 ? w << (23 - 8 * b) : w >> 1;
+  return __uint_as_float(x & 0x7F800000u);
+}
+__device__ __forceinline__ void k_scales(const Frag<4>& f, int b, float& s0, float& s1) {
+  s0 = pow2_bits(f.ks.x, b);
+  s1 = pow2_bits(f.ks.y, b);
+}
+__device__ __forceinline__ void k_scales(const Frag<2>& f, int b, float& s0, float& s1) {
+  s0 = pow2_bits(f.ks, b);
+  s1 = pow2_bits(f.ks, b + 2);
+}
+
+// V scale bytes of the lane's keys (2c, 2c + 1) [h = 0] or (2c + 8, 2c + 9) [h = 1] as 16-bit pairs, block b.
+__device__ __forceinline__ void v_scale_pairs(const Frag<4>& f, uint32_t (&s)[4][2]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t a = h ? f.vs.z : f.vs.x, b = h ? f.vs.w : f.vs.y;
+    const uint32_t lo = __byte_perm(a, b, 0x5410), hi = __byte_perm(a, b, 0x7632);
+    s[0][h] = lo & 0x00FF00FFu;
+    s[1][h] = (lo >> 8) & 0x00FF00FFu;
+    s[2][h] = hi & 0x00FF00FFu;
+    s[3][h] = (hi >> 8) & 0x00FF00FFu;
+  }
+}
+__device__ __forceinline__ void v_scale_pairs(const Frag<2>& f, uint32_t (&s)[2][2]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t a = h ? f.vs.y : f.vs.x;      // halves: keys 2c, 2c + 1; bytes: blocks 0, 1
+    s[0][h] = a & 0x00FF00FFu;
+    s[1][h] = (a >> 8) & 0x00FF00FFu;
+  }
+}
+
+// Where a request's rows and keys are, read once per CTA.
+struct RequestRange {
+  int start, n;            // first row of q, rows
+  int64_t kv, cap;         // kv_len as given (>= 0), and how many keys may be visited at all
+};
+__device__ __forceinline__ RequestRange request_range(const PagedParams& p, int r) {
+  RequestRange q;
+  const int T = static_cast<int>(p.T);
+  q.start = max(0, min(p.q_start[r], T));
+  q.n = max(0, min(min(p.q_start[r + 1], T) - q.start, 0x7FFFFFFF));
+  q.kv = max(p.kv_len[r], 0);
+  q.cap = min(min(q.kv, static_cast<int64_t>(0x7FFFFF00)), min(static_cast<int64_t>(p.table_width) << p.page_shift, p.max_kv));
+  return q;
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kSmallWarps * 32, NT == 1 ? 4 : 2) paged_small_kernel(const PagedParams p, const SplitParams sp) {
+  constexpr int NB = D / 32, kRows = 8 * NT, kPad = D + 4;
+  __shared__ float so[kSmallWarps][kRows][kPad];
+  __shared__ float sm[kSmallWarps][kRows], sl[kSmallWarps][kRows];
+  const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3u;
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
+
+  const int G = p.Hq / p.Hkv;
+  uint32_t u = blockIdx.x;
+  const int split = static_cast<int>(u % sp.splits);
+  u /= sp.splits;
+  const int rt = static_cast<int>(u % sp.row_tiles);
+  u /= sp.row_tiles;
+  const int head = static_cast<int>(u % p.Hkv), r = static_cast<int>(u / p.Hkv);
+  const RequestRange rq = request_range(p, r);
+  const int n_used = min(rq.n, p.max_new);
+  const int used_splits = max(1, static_cast<int>((rq.cap + sp.chunk - 1) / sp.chunk));
+  if (rt * kRows >= n_used * G || split >= used_splits) return;
+
+  // ---- Q: column nt * 8 + g of this lane, channels 32 b + 8 c .. + 7 as four fp16 pairs
+  uint32_t qf[NT][NB][4];
+  float qscale[NT][2];
+  int lim[NT][2];          // keys j < lim are visible to columns 2c, 2c + 1
+  int lim_max = 0, lim_min = 0x7FFFFFFF;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int row = rt * kRows + nt * 8 + static_cast<int>(g);
+    const int i = row / G, h = row - i * G;
+    const bool live = i < n_used;
+    float amax = 0.f;
+    uint4 raw[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      raw[b] = make_uint4(0u, 0u, 0u, 0u);
+      if (live)
+        raw[b] = *reinterpret_cast<const uint4*>(p.q + (rq.start + i) * p.q_token_stride + (head * G + h) * p.q_head_stride + b * 32 + c * 8);
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const uint32_t x = word_of(raw[b], w);
+        amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(x << 16)), fabsf(__uint_as_float(x & 0xFFFF0000u))));
+      }
+    }
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    const int e = min(max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -100), 127);
+    const float mul = __uint_as_float(static_cast<uint32_t>(7 - e + 127) << 23);      // 2^(7 - e)
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const uint32_t x = word_of(raw[b], w);
+        qf[nt][b][w] = pack_half2(__uint_as_float(x << 16) * mul, __uint_as_float(x & 0xFFFF0000u) * mul);
+      }
+    int64_t l64 = p.causal ? rq.kv - rq.n + i + 1 : rq.kv;
+    l64 = live ? max(min(l64, rq.cap), static_cast<int64_t>(0)) : 0;
+    const int mine = static_cast<int>(l64);
+    const float back = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(e - 7 + 127) << 23);
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int from = (2 * c + x) * 4;
+      qscale[nt][x] = __shfl_sync(0xffffffffu, back, from);
+      lim[nt][x] = __shfl_sync(0xffffffffu, mine, from);
+      lim_max = max(lim_max, lim[nt][x]);
+      lim_min = min(lim_min, __shfl_sync(0xffffffffu, live ? 1 : 0, from) ? lim[nt][x] : 0x7FFFFFFF);
+    }
+  }
+  lim_max = __reduce_max_sync(0xffffffffu, lim_max);
+  lim_min = __reduce_min_sync(0xffffffffu, lim_min);
+
+  const int first = static_cast<int>(split * sp.chunk) >> 4;
+  const int stop = (min(lim_max, static_cast<int>(min((split + 1) * sp.chunk, static_cast<int64_t>(0x7FFFFFFF)))) + 15) >> 4;
+  const int32_t* table = p.block_table + static_cast<int64_t>(r) * p.table_width;
+  const int64_t head_bytes = 2ll * cache_chunk_bytes(D, 1u << p.page_shift);
+  const uint32_t page_mask = (1u << p.page_shift) - 1u;
+
+  float o[NT][2 * NB][4];
+  float l[NT][2], m[NT][2], mu[NT][2];       // mu: m, or 0 while the column has seen no key
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+    for (int t = 0; t < 2 * NB; ++t)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) o[nt][t][x] = 0.f;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) { l[nt][x] = 0.f; m[nt][x] = -INFINITY; mu[nt][x] = 0.f; }
+  }
+  int rb[NB];                                 // reference exponent byte of V's channel blocks
+#pragma unroll
+  for (int b = 0; b < NB; ++b) rb[b] = -1;
+
+  // one group ahead in registers, its page looked up one group earlier still
+  auto page_of = [&](int grp) -> int {
+    if (grp >= stop) return -1;
+    const int pg = __ldg(table + ((grp << 4) >> p.page_shift));
+    return static_cast<uint32_t>(pg) < static_cast<uint64_t>(p.n_pages) ? pg : -1;
+  };
+  auto fetch = [&](Frag<NB>& f, int grp, int page) {
+    if (page >= 0)
+      load_frag(f, p.cache + (static_cast<int64_t>(page) * p.Hkv + head) * head_bytes, (static_cast<uint32_t>(grp) << 4) & page_mask, p.page_shift, lane);
+  };
+  int grp = first + static_cast<int>(warp);
+  int page = page_of(grp), page_next = page_of(grp + kSmallWarps);
+  Frag<NB> f, fn;
+  fetch(f, grp, page);
+  for (; grp < stop; grp += kSmallWarps) {
+    fetch(fn, grp + kSmallWarps, page_next);
+    const int page_after = page_of(grp + 2 * kSmallWarps);
+    if (page >= 0) {
+      const int key0 = grp << 4;
+      // ---- S^T: partial scores of each 32-channel block, times the block's scale
+      float s[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) s[nt][x] = 0.f;
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        uint32_t a[4], a8[4];
+        e2m1x8_to_half2(word_of(f.k0, b), a);
+        e2m1x8_to_half2(word_of(f.k1, b), a8);
+        float s0, s1;
+        k_scales(f, b, s0, s1);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float acc[4];
+          mma_f16_zero(acc, a[0], a8[0], a[1], a8[1], qf[nt][b][0], qf[nt][b][1]);
+          mma_f16(acc, a[2], a8[2], a[3], a8[3], qf[nt][b][2], qf[nt][b][3]);
+          s[nt][0] = fmaf(acc[0], s0, s[nt][0]);
+          s[nt][1] = fmaf(acc[1], s0, s[nt][1]);
+          s[nt][2] = fmaf(acc[2], s1, s[nt][2]);
+          s[nt][3] = fmaf(acc[3], s1, s[nt][3]);
+        }
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) s[nt][x] *= qscale[nt][x & 1];
+      if (key0 + 16 > lim_min) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            if (key0 + static_cast<int>(g) + (x >> 1) * 8 >= lim[nt][x & 1]) s[nt][x] = -INFINITY;
+      }
+      // ---- the columns' references: moved only when a score passes one by 7
+      bool up = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) up |= fmaxf(s[nt][x], s[nt][x + 2]) > m[nt][x] + 7.f;
+      if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            float t = fmaxf(s[nt][x], s[nt][x + 2]);
+            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
+            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
+            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
+            const float mn = fmaxf(m[nt][x], t);
+            const float mun = mn == -INFINITY ? 0.f : mn;
+            const float alpha = m[nt][x] == -INFINITY ? 0.f : ex2(m[nt][x] - mun);
+            m[nt][x] = mn;
+            mu[nt][x] = mun;
+            l[nt][x] *= alpha;
+#pragma unroll
+            for (int tt = 0; tt < 2 * NB; ++tt) { o[nt][tt][x] *= alpha; o[nt][tt][x + 2] *= alpha; }
+          }
+      }
+      // ---- p = 2^(x - m + 7), summed in fp32; as fp16 the other way round (key pairs of column g)
+      float pv[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) pv[nt][x] = ex2(s[nt][x] - mu[nt][x & 1] + 7.f);
+        l[nt][0] += pv[nt][0] + pv[nt][2];
+        l[nt][1] += pv[nt][1] + pv[nt][3];
+      }
+      // ---- V's scales relative to the reference exponents
+      uint32_t vs[NB][2];
+      v_scale_pairs(f, vs);
+      if (key0 + 16 > lim_max) {              // tokens behind the end: whatever their bytes say
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t keep = (key0 + 8 * h + 2 * static_cast<int>(c) < lim_max ? 0xFFFFu : 0u) |
+                                (key0 + 8 * h + 2 * static_cast<int>(c) + 1 < lim_max ? 0xFFFF0000u : 0u);
+#pragma unroll
+          for (int b = 0; b < NB; ++b) vs[b][h] &= keep;
+        }
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {        // ... they take the largest exponent there is
+          uint32_t t = max(max(vs[b][0] & 0xFFFFu, vs[b][0] >> 16), max(vs[b][1] & 0xFFFFu, vs[b][1] >> 16));
+          t = max(__reduce_max_sync(0xffffffffu, t), static_cast<uint32_t>(max(rb[b], 0)));
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (key0 + 8 * h + 2 * static_cast<int>(c) >= lim_max) vs[b][h] |= t;
+            if (key0 + 8 * h + 2 * static_cast<int>(c) + 1 >= lim_max) vs[b][h] |= t << 16;
+          }
+        }
+      }
+      // d = s - rb + 14 lies in [0, 15] for scales from 2^-14 to 2 of the reference
+      uint32_t rel[NB][2], out_of_range = 0;
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          rel[b][h] = vs[b][h] - static_cast<uint32_t>(rb[b] - 14) * 0x00010001u;
+          out_of_range |= rel[b][h];
+        }
+      bool wide = false;
+      if (__any_sync(0xffffffffu, (out_of_range & 0xFFF0FFF0u) != 0u)) {
+        // a scale above the reference moves it (O is scaled down); one far below takes the wide path
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          const int t = static_cast<int>(__reduce_max_sync(0xffffffffu, max(max(vs[b][0] & 0xFFFFu, vs[b][0] >> 16), max(vs[b][1] & 0xFFFFu, vs[b][1] >> 16))));
+          const int lo = static_cast<int>(__reduce_min_sync(0xffffffffu, min(min(vs[b][0] & 0xFFFFu, vs[b][0] >> 16), min(vs[b][1] & 0xFFFFu, vs[b][1] >> 16))));
+          if (t > rb[b]) {
+            const float down = rb[b] < 0 ? 0.f : exp2f(static_cast<float>(rb[b] - t));
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) o[nt][2 * b + tt][x] *= down;
+            rb[b] = t;
+          }
+          wide |= lo < rb[b] - 14;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) rel[b][h] = vs[b][h] - static_cast<uint32_t>(rb[b] - 14) * 0x00010001u;
+        }
+      }
+      uint32_t pt[NT][2];
+      if (!wide) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          pt[nt][0] = transpose8x8(pack_half2(pv[nt][0], pv[nt][1]));
+          pt[nt][1] = transpose8x8(pack_half2(pv[nt][2], pv[nt][3]));
+        }
+      } else {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          pt[nt][0] = transpose8x8(pack_bf162(pv[nt][0], pv[nt][1]));
+          pt[nt][1] = transpose8x8(pack_bf162(pv[nt][2], pv[nt][3]));
+        }
+      }
+      // ---- O^T += V^T P^T. Words w of a key pair hold blocks 2w, 2w + 1; nibbles of the two keys are
+      //      brought together so that one cvt gives the pair of one channel.
+#pragma unroll
+      for (int w = 0; w < NB / 2; ++w) {
+        uint32_t ev[2][4], od[2][4];          // [key pair][2 (block & 1) + tile]: rows g and g + 8
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t x = word_of(f.v[2 * h], w), y = word_of(f.v[2 * h + 1], w);
+          e2m1x8_to_half2((x & 0x0F0F0F0Fu) | ((y << 4) & 0xF0F0F0F0u), ev[h]);
+          e2m1x8_to_half2(((x >> 4) & 0x0F0F0F0Fu) | (y & 0xF0F0F0F0u), od[h]);
+        }
+#pragma unroll
+        for (int bb = 0; bb < 2; ++bb) {
+          const int b = 2 * w + bb;
+          if (!wide) {
+            const uint32_t sc0 = rel[b][0] * 1024u + 0x04000400u, sc1 = rel[b][1] * 1024u + 0x04000400u;   // 2^(s - rb)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              const uint32_t b0 = hmul2(pt[nt][0], sc0), b1 = hmul2(pt[nt][1], sc1);
+#pragma unroll
+              for (int t = 0; t < 2; ++t)
+                mma_f16(o[nt][2 * b + t], ev[0][2 * bb + t], od[0][2 * bb + t], ev[1][2 * bb + t], od[1][2 * bb + t], b0, b1);
+            }
+          } else {
+            // bf16 V relative to the reference: code 2^(s - rb), exact; P in bf16
+            uint32_t e2[2][2], o2[2][2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float f0 = exp2f(static_cast<float>(static_cast<int>(vs[b][h] & 0xFFFFu) - rb[b]));
+              const float f1 = exp2f(static_cast<float>(static_cast<int>(vs[b][h] >> 16) - rb[b]));
+#pragma unroll
+              for (int t = 0; t < 2; ++t) {
+                const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&ev[h][2 * bb + t]));
+                const float2 z = __half22float2(*reinterpret_cast<const __half2*>(&od[h][2 * bb + t]));
+                e2[h][t] = pack_bf162(a.x * f0, a.y * f1);
+                o2[h][t] = pack_bf162(z.x * f0, z.y * f1);
+              }
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int t = 0; t < 2; ++t) mma_bf16(o[nt][2 * b + t], e2[0][t], o2[0][t], e2[1][t], o2[1][t], pt[nt][0], pt[nt][1]);
+          }
+        }
+      }
+    }
+    f = fn;
+    page = page_next;
+    page_next = page_after;
+  }
+
+  // ---- the warps' results meet in shared memory
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      float t = l[nt][x];
+      t += __shfl_xor_sync(0xffffffffu, t, 4);
+      t += __shfl_xor_sync(0xffffffffu, t, 8);
+      t += __shfl_xor_sync(0xffffffffu, t, 16);
+      const int row = nt * 8 + 2 * static_cast<int>(c) + x;
+      if (g == 0) {
+        sl[warp][row] = t;
+        sm[warp][row] = m[nt][x];
+      }
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const float unit = rb[b] < 0 ? 0.f : pow2_from_byte(static_cast<uint32_t>(rb[b]));
+        const float4 v = make_float4(o[nt][2 * b][x] * unit, o[nt][2 * b][x + 2] * unit, o[nt][2 * b + 1][x] * unit, o[nt][2 * b + 1][x + 2] * unit);
+        *reinterpret_cast<float4*>(&so[warp][row][32 * b + 4 * g]) = v;
+      }
+    }
+  }
+  __syncthreads();
+  constexpr int kPer = D / 32;
+  for (int row = static_cast<int>(warp); row < kRows; row += kSmallWarps) {
+    const int at = rt * kRows + row;
+    const int i = at / G, h = at - i * G;
+    if (i >= n_used) break;
+    float top = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kSmallWarps; ++w) top = fmaxf(top, sm[w][row]);
+    const float base = top == -INFINITY ? 0.f : top;
+    float sum = 0.f, acc[kPer];
+#pragma unroll
+    for (int x = 0; x < kPer; ++x) acc[x] = 0.f;
+#pragma unroll
+    for (int w = 0; w < kSmallWarps; ++w) {
+      const float k = ex2(sm[w][row] - base);            // 0 for a warp that saw no key
+      sum = fmaf(k, sl[w][row], sum);
+#pragma unroll
+      for (int x = 0; x < kPer; ++x) acc[x] = fmaf(k, so[w][row][lane * kPer + x], acc[x]);
+    }
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const float lse2 = sum > 0.f ? base - 7.f + log2f(sum) : -INFINITY;
+    const int64_t orow = static_cast<int64_t>(rq.start + i) * p.Hq + head * G + h;
+    if (used_splits == 1) {
+#pragma unroll
+      for (int x = 0; x < kPer; x += 2)
+        *reinterpret_cast<uint32_t*>(p.out + orow * D + lane * kPer + x) = pack_bf162(acc[x] * inv, acc[x + 1] * inv);
+      if (p.lse && lane == 0) p.lse[orow] = lse2 * 0.6931471805599453f;
+    } else {
+      float* po = sp.part_o + (orow * sp.splits + split) * D + lane * kPer;
+#pragma unroll
+      for (int x = 0; x < kPer; ++x) po[x] = acc[x] * inv;
+      if (lane == 0) sp.part_lse[orow * sp.splits + split] = lse2;
+    }
+  }
+}
+
+// out = sum over the splits of a row of 2^(lse_s - lse) o_s: one warp per row.
+template <int D>
+__global__ void __launch_bounds__(128) paged_combine_kernel(const PagedParams p, const SplitParams sp) {
+  constexpr int kPer = D / 32;
+  const int lane = threadIdx.x & 31;
   const int64_t unit = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
   const int64_t per_request = static_cast<int64_t>(p.max_new) * p.Hq;
   const int r = static_cast<int>(unit / per_request);
   if (r >= p.R) return;
-  const int i = static_cast<int>((unit - r * per_request) / p.Hq), h = static_cast<int>(unit % p.Hq);
-  const int start = max(0, min(p.q_start[r], static_cast<int>(p.T)));
-  const int n = min(min(p.q_start[r + 1], static_cast<int>(p.T)) - start, p.max_new);
-  if (i >= n) return;
-  const int raw_kv = p.kv_len[r];
-  const int64_t cap = min(static_cast<int64_t>(p.table_width) << p.page_shift, p.max_kv);
-  int64_t last = p.causal ? static_cast<int64_t>(raw_kv) - n + i : static_cast<int64_t>(raw_kv) - 1;
-  last = min(last, cap - 1);
-  const int head = h / (p.Hq / p.Hkv);
-  const int64_t row = static_cast<int64_t>(start + i);
-  float q[C], o[C], m = -INFINITY, l = 0.f;
+  const int64_t rest = unit - r * per_request;
+  const int i = static_cast<int>(rest / p.Hq), h = static_cast<int>(rest % p.Hq);
+  const RequestRange rq = request_range(p, r);
+  const int used = static_cast<int>((rq.cap + sp.chunk - 1) / sp.chunk);
+  if (i >= rq.n || used <= 1) return;
+  const int64_t orow = static_cast<int64_t>(rq.start + i) * p.Hq + h;
+  const float* lse = sp.part_lse + orow * sp.splits;
+  const float* po = sp.part_o + orow * sp.splits * D + lane * kPer;
+  float top = -INFINITY;
+  for (int s = lane; s < used; s += 32) top = fmaxf(top, lse[s]);
 #pragma unroll
-  for (int c = 0; c < C; ++c) {
-    q[c] = __bfloat162float(p.q[row * p.q_token_stride + h * p.q_head_stride + lane * C + c]) * p.scale_log2;
-    o[c] = 0.f;
+  for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+  const float base = top == -INFINITY ? 0.f : top;
+  float sum = 0.f, acc[kPer];
+#pragma unroll
+  for (int x = 0; x < kPer; ++x) acc[x] = 0.f;
+#pragma unroll 4
+  for (int s = 0; s < used; ++s) {
+    const float k = ex2(lse[s] - base);
+    sum += k;
+#pragma unroll
+    for (int x = 0; x < kPer; ++x) acc[x] = fmaf(k, po[static_cast<int64_t>(s) * D + x], acc[x]);
   }
-  const int64_t chunk = cache_chunk_bytes(D, 1u << p.page_shift);
-  for (int64_t j = 0; j <= last; ++j) {
-    const int page = p.block_table[static_cast<int64_t>(r) * p.table_width + (j >> p.page_shift)];
-    if (page < 0 || page >= p.n_pages) continue;            // a page that is not there: its keys are masked
-    const uint8_t* kc = p.cache + (static_cast<int64_t>(page) * p.Hkv + head) * 2 * chunk;
-    const uint32_t off = static_cast<uint32_t>(j & ((1ll << p.page_shift) - 1));
-    float s = 0.f;
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
 #pragma unroll
-    for (int c = 0; c < C; ++c) s += q[c] * cache_value<D>(kc, off, lane * C + c, 0, p.page_shift);
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    const float mn = fmaxf(m, s), a = exp2f(m - mn), w = exp2f(s - mn);
-    l = l * a + w;
-#pragma unroll
-    for (int c = 0; c < C; ++c) o[c] = o[c] * a + w * cache_value<D>(kc + chunk, off, lane * C + c, 1, p.page_shift);
-    m = mn;
-  }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-#pragma unroll
-  for (int c = 0; c < C; ++c) p.out[(row * p.Hq + h) * D + lane * C + c] = __float2bfloat16_rn(o[c] * inv);
-  if (p.lse && lane == 0) p.lse[row * p.Hq + h] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+  for (int x = 0; x < kPer; x += 2)
+    *reinterpret_cast<uint32_t*>(p.out + orow * D + lane * kPer + x) = pack_bf162(acc[x] * inv, acc[x + 1] * inv);
+  if (p.lse && lane == 0) p.lse[orow] = sum > 0.f ? (base + log2f(sum)) * 0.6931471805599453f : -INFINITY;
 }
 
-cudaError_t launch_paged(const PagedParams& p, int d, cudaStream_t stream) {
-  const int64_t units = static_cast<int64_t>(p.R) * p.max_new * p.Hq;
-  const unsigned grid = static_cast<unsigned>((units + 3) / 4);
-  if (d == 128) paged_simple_kernel<128><<<grid, 128, 0, stream>>>(p);
-  else paged_simple_kernel<64><<<grid, 128, 0, stream>>>(p);
+SplitPlan plan_splits(int64_t T, int R, int Hq, int Hkv, int d, int max_new, int64_t max_kv) {
+  SplitPlan s{};
+  const int64_t G = Hq / Hkv;
+  const int64_t rows = static_cast<int64_t>(max_new) * G;
+  s.nt = rows <= 8 ? 1 : 2;
+  s.row_tiles = (rows + 8 * s.nt - 1) / (8 * s.nt);
+  const int64_t units = static_cast<int64_t>(R) * Hkv * s.row_tiles;
+  int64_t chunk = (units * max_kv + 1183) / 1184;            // about two CTAs for each of 148 x 4 places
+  chunk = (chunk + 63) / 64 * 64;
+  if (chunk < 64) chunk = 64;
+  int64_t splits = (max_kv + chunk - 1) / chunk;
+  if (splits > 128) {
+    chunk = ((max_kv + 127) / 128 + 63) / 64 * 64;
+    splits = (max_kv + chunk - 1) / chunk;
+  }
+  s.chunk = chunk;
+  s.splits = splits < 1 ? 1 : splits;
+  s.units = units * s.splits;
+  s.part_rows = s.splits > 1 ? T * Hq * s.splits : 0;
+  return s;
+}
+
+template <int D>
+static cudaError_t launch_small(const PagedParams& p, const SplitParams& sp, const SplitPlan& s, cudaStream_t stream) {
+  if (s.nt == 1) paged_small_kernel<D, 1><<<static_cast<unsigned>(s.units), kSmallWarps * 32, 0, stream>>>(p, sp);
+  else paged_small_kernel<D, 2><<<static_cast<unsigned>(s.units), kSmallWarps * 32, 0, stream>>>(p, sp);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || s.splits == 1) return e;
+  const int64_t rows = static_cast<int64_t>(p.R) * p.max_new * p.Hq;
+  paged_combine_kernel<D><<<static_cast<unsigned>((rows + 3) / 4), 128, 0, stream>>>(p, sp);
   return cudaGetLastError();
+}
+
+cudaError_t launch_paged(const PagedParams& p, const SplitPlan& s, void* part, int d, cudaStream_t stream) {
+  SplitParams sp{};
+  sp.chunk = s.chunk;
+  sp.splits = static_cast<uint32_t>(s.splits);
+  sp.row_tiles = static_cast<uint32_t>(s.row_tiles);
+  sp.part_o = static_cast<float*>(part);
+  sp.part_lse = sp.part_o + s.part_rows * d;
+  return d == 128 ? launch_small<128>(p, sp, s, stream) : launch_small<64>(p, sp, s, stream);
 }
 
 }  // namespace mxattn
