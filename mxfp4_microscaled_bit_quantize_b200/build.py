@@ -11,7 +11,7 @@ ROOT = os.path.dirname(PKG_DIR)
 CSRC = os.path.join(PKG_DIR, "csrc")
 LIB_PATH = os.path.join(PKG_DIR, "libmxattn.so")
 SOURCES = ["quantize.cu", "attn_fwd_sm100.cu", "gemm_sm100.cu", "mxattn_api.cu", "mxattn_noalloc.cu", "selftest.cu",
-           "paged_cache.cu", "paged_attn.cu", "paged_api.cu"]
+           "paged_cache.cu", "paged_attn.cu", "paged_attn_sm100.cu", "paged_api.cu"]
 ARCH_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

@@ -183,7 +183,8 @@ struct PagedParams {
 };
 // How the work of a call is laid out, from the host's bounds alone.
 struct SplitPlan {
-  int nt;                  // 8-column tiles of query rows per CTA
+  int tc;                  // tcgen05 kernel (row tiles of 256) instead of the mma.sync one
+  int nt;                  // mma.sync: 8-column tiles of query rows per CTA
   int64_t row_tiles, chunk, splits, units;
   int64_t part_rows;       // partial rows in the workspace (0: one split)
 };
@@ -194,6 +195,7 @@ struct SplitParams {
   float* part_o;           // [T, Hq, splits, d] normalised partial rows
   float* part_lse;         // [T, Hq, splits] log2 of their sums
 };
+cudaError_t launch_paged_tc(const PagedParams& p, const SplitParams& sp, int d, int64_t units, cudaStream_t stream);
 cudaError_t launch_paged(const PagedParams& p, const SplitPlan& s, void* part, int d, cudaStream_t stream);
 
 // Status codes written by kernels into the workspace status word.

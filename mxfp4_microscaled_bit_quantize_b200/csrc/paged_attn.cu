@@ -27,9 +27,7 @@
 #include <cmath>
 #include <cstdint>
 
-#include "cache_layout.cuh"
-#include "mxattn_internal.h"
-#include "sm100_ptx.cuh"
+#include "paged_common.cuh"
 
 namespace mxattn {
 
@@ -38,22 +36,6 @@ constexpr int kSmallWarps = 4;
 template <int NB> struct Frag;          // what a lane holds of 16 keys
 template <> struct Frag<4> { uint4 k0, k1; uint2 ks; uint2 v[4]; uint4 vs; };
 template <> struct Frag<2> { uint2 k0, k1; uint32_t ks; uint32_t v[4]; uint2 vs; };
-
-__device__ __forceinline__ uint4 ldg16(const uint8_t* p) {
-  uint4 r;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
-  return r;
-}
-__device__ __forceinline__ uint2 ldg8(const uint8_t* p) {
-  uint2 r;
-  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
-  return r;
-}
-__device__ __forceinline__ uint32_t ldg4(const uint8_t* p) {
-  uint32_t r;
-  asm volatile("ld.global.nc.L1::no_allocate.u32 %0, [%1];" : "=r"(r) : "l"(p));
-  return r;
-}
 
 // kc: the page's K chunk of this head; off: first of the 16 tokens in the page.
 __device__ __forceinline__ void load_frag(Frag<4>& f, const uint8_t* kc, uint32_t off, int page_shift, uint32_t lane) {
@@ -104,30 +86,11 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
 }
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ uint32_t pack_bf162(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-
-__device__ __forceinline__ uint32_t word_of(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
-__device__ __forceinline__ uint32_t word_of(const uint2& v, int i) { return i == 0 ? v.x : v.y; }
-__device__ __forceinline__ uint32_t word_of(uint32_t v, int) { return v; }
 
 // Scale bytes of block b for the lane's keys g and g + 8 as fp32 powers of two (byte 0 becomes 0).
 __device__ __forceinline__ float pow2_bits(uint32_t w, int b) {
@@ -162,21 +125,6 @@ __device__ __forceinline__ void v_scale_pairs(const Frag<2>& f, uint32_t (&s)[2]
     s[0][h] = a & 0x00FF00FFu;
     s[1][h] = (a >> 8) & 0x00FF00FFu;
   }
-}
-
-// Where a request's rows and keys are, read once per CTA.
-struct RequestRange {
-  int start, n;            // first row of q, rows
-  int64_t kv, cap;         // kv_len as given (>= 0), and how many keys may be visited at all
-};
-__device__ __forceinline__ RequestRange request_range(const PagedParams& p, int r) {
-  RequestRange q;
-  const int T = static_cast<int>(p.T);
-  q.start = max(0, min(p.q_start[r], T));
-  q.n = max(0, min(min(p.q_start[r + 1], T) - q.start, 0x7FFFFFFF));
-  q.kv = max(p.kv_len[r], 0);
-  q.cap = min(min(q.kv, static_cast<int64_t>(0x7FFFFF00)), min(static_cast<int64_t>(p.table_width) << p.page_shift, p.max_kv));
-  return q;
 }
 
 template <int D, int NT>
@@ -574,19 +522,26 @@ __global__ void __launch_bounds__(128) paged_combine_kernel(const PagedParams p,
   if (p.lse && lane == 0) p.lse[orow] = sum > 0.f ? (base + log2f(sum)) * 0.6931471805599453f : -INFINITY;
 }
 
+// Up to 16 rows (new tokens x heads of a group) go to the mma.sync kernel, whose time does not depend on
+// rows that are not there; more rows share the tcgen05 kernel's conversion of the keys.
 SplitPlan plan_splits(int64_t T, int R, int Hq, int Hkv, int d, int max_new, int64_t max_kv) {
   SplitPlan s{};
-  const int64_t G = Hq / Hkv;
-  const int64_t rows = static_cast<int64_t>(max_new) * G;
+  const int64_t rows = static_cast<int64_t>(max_new) * (Hq / Hkv);
+  s.tc = rows > 16;
   s.nt = rows <= 8 ? 1 : 2;
-  s.row_tiles = (rows + 8 * s.nt - 1) / (8 * s.nt);
+  const int64_t per = s.tc ? 256 : 8 * s.nt;
+  const int64_t unit = s.tc ? 128 : 64;                      // chunks are multiples of this many keys
+  s.row_tiles = (rows + per - 1) / per;
   const int64_t units = static_cast<int64_t>(R) * Hkv * s.row_tiles;
-  int64_t chunk = (units * max_kv + 1183) / 1184;            // about two CTAs for each of 148 x 4 places
-  chunk = (chunk + 63) / 64 * 64;
-  if (chunk < 64) chunk = 64;
+  int64_t chunk;
+  if (s.tc) chunk = units >= 592 ? max_kv : (units * max_kv + 887) / 888;      // six CTAs for each SM, or four without splits
+  else chunk = (units * max_kv + 1183) / 1184;               // two CTAs for each of 148 x 4 places
+  if (s.tc && chunk < 1024) chunk = 1024;
+  chunk = (chunk + unit - 1) / unit * unit;
+  if (chunk < unit) chunk = unit;
   int64_t splits = (max_kv + chunk - 1) / chunk;
   if (splits > 128) {
-    chunk = ((max_kv + 127) / 128 + 63) / 64 * 64;
+    chunk = ((max_kv + 127) / 128 + unit - 1) / unit * unit;
     splits = (max_kv + chunk - 1) / chunk;
   }
   s.chunk = chunk;
@@ -597,10 +552,15 @@ SplitPlan plan_splits(int64_t T, int R, int Hq, int Hkv, int d, int max_new, int
 }
 
 template <int D>
-static cudaError_t launch_small(const PagedParams& p, const SplitParams& sp, const SplitPlan& s, cudaStream_t stream) {
-  if (s.nt == 1) paged_small_kernel<D, 1><<<static_cast<unsigned>(s.units), kSmallWarps * 32, 0, stream>>>(p, sp);
-  else paged_small_kernel<D, 2><<<static_cast<unsigned>(s.units), kSmallWarps * 32, 0, stream>>>(p, sp);
-  cudaError_t e = cudaGetLastError();
+static cudaError_t launch_rows(const PagedParams& p, const SplitParams& sp, const SplitPlan& s, cudaStream_t stream) {
+  cudaError_t e;
+  if (s.tc) {
+    e = launch_paged_tc(p, sp, D, s.units, stream);
+  } else {
+    if (s.nt == 1) paged_small_kernel<D, 1><<<static_cast<unsigned>(s.units), kSmallWarps * 32, 0, stream>>>(p, sp);
+    else paged_small_kernel<D, 2><<<static_cast<unsigned>(s.units), kSmallWarps * 32, 0, stream>>>(p, sp);
+    e = cudaGetLastError();
+  }
   if (e != cudaSuccess || s.splits == 1) return e;
   const int64_t rows = static_cast<int64_t>(p.R) * p.max_new * p.Hq;
   paged_combine_kernel<D><<<static_cast<unsigned>((rows + 3) / 4), 128, 0, stream>>>(p, sp);
@@ -614,7 +574,7 @@ cudaError_t launch_paged(const PagedParams& p, const SplitPlan& s, void* part, i
   sp.row_tiles = static_cast<uint32_t>(s.row_tiles);
   sp.part_o = static_cast<float*>(part);
   sp.part_lse = sp.part_o + s.part_rows * d;
-  return d == 128 ? launch_small<128>(p, sp, s, stream) : launch_small<64>(p, sp, s, stream);
+  return d == 128 ? launch_rows<128>(p, sp, s, stream) : launch_rows<64>(p, sp, s, stream);
 }
 
 }  // namespace mxattn

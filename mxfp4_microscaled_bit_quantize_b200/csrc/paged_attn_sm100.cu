@@ -1,0 +1,535 @@
+// Attention of many new tokens over the paged MXFP4 KV cache (chunks of prompts, cross attention):
+// tcgen05 products in bf16 with K and V tiles made from the pages on the way to shared memory.
+//
+//   S = Q K^T;  m' = max(m, rowmax S c),  c = log2(e) / sqrt(d);  P = 2^(S c - m');
+//   O = 2^(m - m') O + P V;  l = 2^(m - m') l + rowsum P;  out = O / l
+//
+// Bound: 4 d FLOP per (query head, key) on the tensor cores, next to one exponential (MUFU: 16 per
+// clock and SM) per (query head, key): for d = 128 and 256 query rows both need about 2100 clocks per
+// 128 keys. The conversion of the 128 keys (E2M1 times a power of two is exact in bf16) costs about
+// 800 issue slots per SM sub-partition, so a CTA owns 256 query rows to share it.
+//
+// Work unit: one CTA (one per SM: it takes all 512 TMEM columns) owns 256 consecutive rows (token,
+// query head of the group) of one request and KV head, as two tiles A and B of 128, and visits the
+// keys of one split in tiles of 128. 512 threads:
+//   warps 0, 1   issue the products of tile A, B (one thread each): S(t) into TMEM, then P V(t) with P
+//                as the TMEM operand, then S(t + 1) over the same columns, each after the commit of the
+//                one before; the two tiles' products fill each other's gaps
+//   warps 4-7    convert: page lookups and code loads one tile ahead in registers, then K(t) and V(t)
+//                as bf16 into a two-stage ring (128-byte swizzle: K is K-major, V MN-major)
+//   warps 8-15   softmax of tiles A and B, one thread per row; O is rescaled in TMEM only when a row's
+//                maximum passes its reference by 8 (P <= 2^8 is bf16's business as usual)
+// P is rounded to bf16 (8 bits) for the product, the row sum is taken before the rounding, in fp32.
+#include <cuda_bf16.h>
+#include <cstdint>
+
+#include "paged_common.cuh"
+
+namespace mxattn {
+
+namespace {
+
+constexpr int kTcThreads = 512, kTcLaunchRegs = 128;
+constexpr int kIssueRegs = 56, kConvRegs = 88, kRowRegs = 184;
+static_assert(kIssueRegs + kConvRegs + 2 * kRowRegs == 4 * kTcLaunchRegs, "register split");
+constexpr uint32_t kTcCols = 512, kColSx = 0, kColOx = 256;   // S / P of tile X at 128 X, O at 256 + 128 X
+constexpr uint32_t kSw128 = 2;                                // descriptor code of the 128-byte swizzle
+constexpr int kTcStages = 2;
+
+template <int D>
+struct __align__(1024) TcSmem {
+  static constexpr int kTile = 128 * D * 2;      // 128 rows of D bf16, as D / 64 slabs of 128 x 128 bytes
+  uint8_t q[2][kTile];
+  uint8_t k[kTcStages][kTile];
+  uint8_t v[kTcStages][kTile];
+  uint64_t bar_q;
+  uint64_t bar_k_full[kTcStages], bar_v_full[kTcStages], bar_k_empty[kTcStages], bar_v_empty[kTcStages];
+  uint64_t bar_s_full[2], bar_p_full[2], bar_pv[2], bar_drain[2];
+  uint32_t tmem_base;
+  int abort_flag;
+};
+
+// Instruction descriptor, kind::f16: bf16 operands, fp32 accumulator, M = 128; B MN-major or K-major.
+__host__ __device__ constexpr uint32_t idesc_bf16(uint32_t n, uint32_t b_mn_major) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (b_mn_major << 16) | ((n >> 3) << 17) | ((128u >> 4) << 24);
+}
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+               "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+}
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+               "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+}
+
+__device__ __forceinline__ bool warp_wait_tc(uint64_t* bar, uint32_t parity, volatile int* abort_flag, unsigned int* status, unsigned int code) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status, code));
+}
+__device__ __forceinline__ void drain_wait_tc(uint64_t* bar, uint32_t parity) {
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_try_wait(bar, parity))
+    if (global_timer_ns() - t0 > 200ull * 1000ull * 1000ull) break;
+}
+
+__device__ __forceinline__ uint32_t mul_bf162(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Eight codes times 2^(s - 127) as bf16, in the order e0 e4 e1 e5 e2 e6 e3 e7. A nibble (s eem) shifted
+// to the sign and to the three bits at the border of bf16's exponent and mantissa is the code's value
+// times 2^-126, exactly (code 1, E2M1's subnormal, becomes a bf16 subnormal), so one product by
+// 2^(s - 1) finishes it; scales above 2 need a second one, since 2^(s - 1) leaves bf16's range there.
+__device__ __forceinline__ void codes_to_bf16(uint32_t w, uint32_t s, uint32_t (&r)[4]) {
+  const uint32_t mul = (min(s, 128u) + 126u) * 0x00800080u;
+  const uint32_t t[4] = {w << 12, w << 8, w << 4, w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) r[j] = mul_bf162(((t[j] >> 6) & 0x01C001C0u) | (t[j] & 0x80008000u), mul);
+  if (s > 128u) {
+    const uint32_t more = (s - 1u) * 0x00800080u;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r[j] = mul_bf162(r[j], more);
+  }
+}
+
+// What a converting lane holds of a tile's K or V: piece (lane & 3) of rows (lane >> 2) + 8 i of its
+// warp's 32, and those rows' scale bytes.
+template <int D> struct Raw;
+template <> struct Raw<128> { uint4 w[4]; uint32_t s[4]; };
+template <> struct Raw<64> { uint2 w[4]; uint32_t s[4]; };
+
+__device__ __forceinline__ void clear(uint4& v) { v = make_uint4(0u, 0u, 0u, 0u); }
+__device__ __forceinline__ void clear(uint2& v) { v = make_uint2(0u, 0u); }
+__device__ __forceinline__ void load_piece(uint4& v, const uint8_t* p) { v = ldg16(p); }
+__device__ __forceinline__ void load_piece(uint2& v, const uint8_t* p) { v = ldg8(p); }
+template <int D>
+__device__ __forceinline__ uint32_t load_scales(const uint8_t* p) {
+  if constexpr (D == 128) return ldg4(p);
+  uint16_t r;
+  asm volatile("ld.global.nc.L1::no_allocate.u16 %0, [%1];" : "=h"(r) : "l"(p));
+  return r;
+}
+
+// Word c of each block of a row, from the row's piece c.
+template <int W>
+__device__ __forceinline__ void block_words(const uint4& o, uint32_t (&q)[4]) {
+  if (W == 0) { q[0] = o.x; q[1] = o.y; q[2] = o.z; q[3] = o.w; }
+  else { q[0] = lo16x2(o.x, o.z); q[1] = hi16x2(o.x, o.z); q[2] = lo16x2(o.y, o.w); q[3] = hi16x2(o.y, o.w); }
+}
+template <int W>
+__device__ __forceinline__ void block_words(const uint2& o, uint32_t (&q)[2]) {
+  if (W == 0) { q[0] = o.x; q[1] = o.y; }
+  else { q[0] = lo16x2(o.x, o.y); q[1] = hi16x2(o.x, o.y); }
+}
+
+// Rows of a tile into shared memory: 16-byte column j of row r in slab j / 8 at (j % 8) ^ (r % 8).
+// Lanes of odd rows take the blocks of a pair in the other order, so that the eight lanes of a store
+// phase (two rows, four pieces) cover all banks.
+template <int D, int W>
+__device__ __forceinline__ void store_rows(const Raw<D>& raw, uint32_t tile, uint32_t row0, uint32_t lane) {
+  constexpr int NB = D / 32;
+  const uint32_t c = lane & 3u, odd = (lane >> 2) & 1u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t row = row0 + 8u * i + (lane >> 2);
+    uint32_t q[NB];
+    block_words<W>(raw.w[i], q);
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const uint32_t bx = static_cast<uint32_t>(b) ^ odd;
+      const uint32_t w = odd ? q[b ^ 1] : q[b];
+      uint32_t r[4];
+      codes_to_bf16(w, (raw.s[i] >> (8u * bx)) & 0xFFu, r);
+      const uint32_t col = 4u * bx + c;
+      st_shared_v4(tile + (col >> 3) * (128u * 128u) + row * 128u + (((col ^ row) & 7u) << 4), r[0], r[1], r[2], r[3]);
+    }
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const PagedParams p, const SplitParams sp) {
+  constexpr int NB = D / 32;
+  using Sm = TcSmem<D>;
+  extern __shared__ uint8_t smem_raw[];
+  Sm& s = *reinterpret_cast<Sm*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  // ---- work unit
+  const int G = p.Hq / p.Hkv;
+  uint32_t u = blockIdx.x;
+  const int split = static_cast<int>(u % sp.splits);
+  u /= sp.splits;
+  const int pair = static_cast<int>(sp.row_tiles - 1 - u % sp.row_tiles);   // causal: longest first
+  u /= sp.row_tiles;
+  const int head = static_cast<int>(u % p.Hkv), r = static_cast<int>(u / p.Hkv);
+  const RequestRange rq = request_range(p, r);
+  const int n_used = min(rq.n, p.max_new);
+  const int rows_all = n_used * G;
+  const int used_splits = max(1, static_cast<int>((rq.cap + sp.chunk - 1) / sp.chunk));
+  if (pair * 256 >= rows_all || split >= used_splits) return;
+  auto limit_of = [&](int row) -> int64_t {                   // keys j < limit are visible to the row
+    const int64_t l = p.causal ? rq.kv - rq.n + row / G + 1 : rq.kv;
+    return max(min(l, rq.cap), static_cast<int64_t>(0));
+  };
+  const int64_t key_begin = split * sp.chunk;
+  int n_x[2];
+  int64_t lim_all = 0;
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const int first = pair * 256 + x * 128, last = min(rows_all, first + 128) - 1;
+    const int64_t lim = first < rows_all ? min(limit_of(last), key_begin + sp.chunk) : 0;
+    n_x[x] = lim > key_begin ? static_cast<int>((lim - key_begin + 127) >> 7) : 0;
+    lim_all = max(lim_all, lim);
+  }
+  const int n_max = max(n_x[0], n_x[1]);
+
+  if (threadIdx.x == 0) {
+    mbar_init(&s.bar_q, 8);
+    for (int i = 0; i < kTcStages; ++i) {
+      mbar_init(&s.bar_k_full[i], 4);
+      mbar_init(&s.bar_v_full[i], 4);
+      mbar_init(&s.bar_k_empty[i], 2);
+      mbar_init(&s.bar_v_empty[i], 2);
+    }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&s.bar_s_full[x], 1);
+      mbar_init(&s.bar_p_full[x], 4);
+      mbar_init(&s.bar_pv[x], 1);
+      mbar_init(&s.bar_drain[x], 1);
+    }
+    s.abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(&s.tmem_base, kTcCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s.tmem_base;
+  volatile int* abort_flag = &s.abort_flag;
+
+  if (warp < 4) {
+    regs_dec<kIssueRegs>();
+    if (warp < 2) {
+      // ======================= products of tile x =======================
+      const int x = warp;
+      const int n_own = x == 0 ? n_x[0] : n_x[1], n_other = x == 0 ? n_x[1] : n_x[0];
+      const bool leader = elect_one_sync();
+      const uint64_t d_k = smem_desc(0, 0, 1024, kSw128);                 // K-major: 8 rows are 1 KB
+      const uint64_t d_v = smem_desc(0, 128 * 128, 1024, kSw128);         // MN-major: slabs 16 KB apart, 8 keys 1 KB
+      const uint32_t a_q = smem_u32(s.q[x]) >> 4, a_k = smem_u32(s.k[0]) >> 4, a_v = smem_u32(s.v[0]) >> 4;
+      const uint32_t t_s = tmem + kColSx + 128 * x, t_o = tmem + kColOx + 128 * x;
+      bool ok = n_own == 0 || warp_wait_tc(&s.bar_q, 0, abort_flag, p.status, kStatusTimeoutQ);
+      auto issue_s = [&](int t) -> bool {
+        const int st = t % kTcStages;
+        if (!warp_wait_tc(&s.bar_k_full[st], (t / kTcStages) & 1, abort_flag, p.status, kStatusTimeoutKV | st)) return false;
+        tc_fence_after();
+        if (leader) {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t at = (kk >> 2) * 1024u + (kk & 3) * 2u;         // slab, 32 bytes per 16 channels
+            tc_mma_ss(t_s, d_k | (a_q + at), d_k | (a_k + st * (Sm::kTile >> 4) + at), idesc_bf16(128, 0), kk > 0);
+          }
+          tc_commit(&s.bar_s_full[x]);
+          tc_commit(&s.bar_k_empty[st]);
+          if (t >= n_other) mbar_arrive(&s.bar_k_empty[st]);               // the other tile has no product here
+        }
+        __syncwarp();
+        return true;
+      };
+      if (ok && n_own > 0) ok = issue_s(0);
+      for (int t = 0; ok && t < n_own; ++t) {
+        const int st = t % kTcStages;
+        ok = warp_wait_tc(&s.bar_p_full[x], t & 1, abort_flag, p.status, kStatusTimeoutP | x) &&
+             warp_wait_tc(&s.bar_v_full[st], (t / kTcStages) & 1, abort_flag, p.status, kStatusTimeoutKV | 8 | st);
+        if (!ok) break;
+        tc_fence_after();
+        if (leader) {
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            tc_mma_ts(t_o, t_s + 8 * kk, d_v | (a_v + st * (Sm::kTile >> 4) + kk * 128u), idesc_bf16(D, 1), t > 0 || kk > 0);
+          tc_commit(&s.bar_pv[x]);
+          tc_commit(&s.bar_v_empty[st]);
+          if (t >= n_other) mbar_arrive(&s.bar_v_empty[st]);
+        }
+        __syncwarp();
+        if (t + 1 < n_own) {
+          // S(t + 1) overwrites the columns that hold P(t)
+          ok = warp_wait_tc(&s.bar_pv[x], t & 1, abort_flag, p.status, kStatusTimeoutPV | x) && issue_s(t + 1);
+        }
+      }
+      // everything issued above must complete before TMEM is released
+      if (leader) {
+        tc_commit(&s.bar_drain[x]);
+        drain_wait_tc(&s.bar_drain[x], 0);
+      }
+      __syncwarp();
+    }
+  } else if (warp < 8) {
+    regs_dec<kConvRegs>();
+    // ======================= conversion: pages -> bf16 tiles =======================
+    const uint32_t row0 = static_cast<uint32_t>(warp - 4) * 32u, g8 = static_cast<uint32_t>(lane) >> 2, c = lane & 3;
+    const uint32_t shift = p.page_shift, page_mask = (1u << shift) - 1u;
+    const uint32_t codes = static_cast<uint32_t>(D / 2) << shift;         // bytes of codes in a chunk
+    const uint32_t chunk = codes + (static_cast<uint32_t>(NB) << shift);
+    const uint64_t page_stride = static_cast<uint64_t>(p.Hkv) * 2u * chunk;
+    const uint8_t* base = p.cache + static_cast<uint64_t>(head) * 2u * chunk;
+    const int32_t* table = p.block_table + static_cast<int64_t>(r) * p.table_width;
+    // pages of this warp's two groups of 16 keys in tile t (-1: none)
+    auto pages_of = [&](int t, int (&pg)[2]) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int64_t key = key_begin + t * 128ll + row0 + 16 * j;
+        pg[j] = -1;
+        if (t < n_max && key < lim_all) {
+          const int v = __ldg(table + (key >> shift));
+          if (v >= 0 && v < p.n_pages) pg[j] = v;
+        }
+      }
+    };
+    auto load = [&](Raw<D>& raw, int t, const int (&pg)[2], int which) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int64_t key = key_begin + t * 128ll + row0 + 8 * i + g8;
+        clear(raw.w[i]);
+        raw.s[i] = 0;
+        if (pg[i >> 1] >= 0 && key < lim_all) {
+          const uint32_t off = static_cast<uint32_t>(key) & page_mask, o16 = off & ~15u;
+          const uint8_t* ch = base + static_cast<uint32_t>(pg[i >> 1]) * page_stride + which * chunk;
+          load_piece(raw.w[i], ch + off * (D / 2) + c * (D / 8));
+          const uint32_t i16 = g8 + 8u * (i & 1);
+          raw.s[i] = load_scales<D>(ch + codes + (o16 + (which ? v_scale_row(i16) : k_scale_row(i16))) * NB);
+        }
+      }
+    };
+    Raw<D> rk, rv;
+    int pg[2], pg_next[2];
+    pages_of(0, pg);
+    pages_of(1, pg_next);
+    if (n_max > 0) {
+      load(rk, 0, pg, 0);
+      load(rv, 0, pg, 1);
+    }
+    bool ok = true;
+    for (int t = 0; ok && t < n_max; ++t) {
+      const int st = t % kTcStages;
+      const uint32_t par = ((t / kTcStages) & 1) ^ 1;
+      int pg_after[2];
+      pages_of(t + 2, pg_after);
+      if (t >= kTcStages) ok = warp_wait_tc(&s.bar_k_empty[st], par, abort_flag, p.status, kStatusTimeoutEmpty | st);
+      if (!ok) break;
+      store_rows<D, 0>(rk, smem_u32(s.k[st]), row0, lane);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.bar_k_full[st]);
+      if (t + 1 < n_max) load(rk, t + 1, pg_next, 0);
+      if (t >= kTcStages) ok = warp_wait_tc(&s.bar_v_empty[st], par, abort_flag, p.status, kStatusTimeoutEmpty | 8 | st);
+      if (!ok) break;
+      store_rows<D, 1>(rv, smem_u32(s.v[st]), row0, lane);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.bar_v_full[st]);
+      if (t + 1 < n_max) load(rv, t + 1, pg_next, 1);
+      pg_next[0] = pg_after[0];
+      pg_next[1] = pg_after[1];
+    }
+  } else {
+    regs_inc<kRowRegs>();
+    // ======================= softmax: one thread per row =======================
+    const int x = (warp - 8) >> 2, quarter = warp & 3;
+    const int in_tile = quarter * 32 + lane;
+    const int row = pair * 256 + x * 128 + in_tile;
+    const int i = row / G, h = row - i * G;
+    const bool live = row < rows_all;
+    const int n = x == 0 ? n_x[0] : n_x[1];
+    // Q row into shared memory, each 8 channels in the order of the converted codes
+    if (n > 0) {
+      const __nv_bfloat16* src = p.q + (rq.start + (live ? i : 0)) * p.q_token_stride + (head * G + h) * p.q_head_stride;
+      const uint32_t tile = smem_u32(s.q[x]);
+#pragma unroll
+      for (int j = 0; j < D / 8; ++j) {
+        uint4 w = make_uint4(0u, 0u, 0u, 0u);
+        if (live) w = *reinterpret_cast<const uint4*>(src + j * 8);
+        st_shared_v4(tile + (j >> 3) * (128u * 128u) + in_tile * 128u + (((j ^ in_tile) & 7) << 4), lo16x2(w.x, w.z), hi16x2(w.x, w.z), lo16x2(w.y, w.w),
+                     hi16x2(w.y, w.w));
+      }
+      fence_proxy_async_smem();
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&s.bar_q);
+
+    const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t t_s = tmem + lane_addr + kColSx + 128 * x, t_o = tmem + lane_addr + kColOx + 128 * x;
+    const float c = p.scale_log2;
+    const int lim = live ? static_cast<int>(max(limit_of(row) - key_begin, static_cast<int64_t>(0))) : 0;   // in the split
+    const uint32_t shift = p.page_shift;
+    const int32_t* table = p.block_table + static_cast<int64_t>(r) * p.table_width;
+    // lane j < 8 looks after keys 16 j .. 16 j + 15 of a tile: is their page there?
+    auto missing = [&](int t) -> bool {
+      const int64_t key = key_begin + t * 128ll + lane * 16;
+      if (t >= n || lane >= 8 || key >= lim_all) return false;
+      const int v = __ldg(table + (key >> shift));
+      return v < 0 || v >= p.n_pages;
+    };
+    float m = -INFINITY, mu = 0.f, l0 = 0.f, l1 = 0.f;
+    bool miss = missing(0);
+    bool ok = true;
+    for (int t = 0; ok && t < n; ++t) {
+      const uint32_t gone = __ballot_sync(0xffffffffu, miss);
+      miss = missing(t + 1);
+      ok = warp_wait_tc(&s.bar_s_full[x], t & 1, abort_flag, p.status, kStatusTimeoutS | x);
+      if (!ok) break;
+      tc_fence_after();
+      float v[128];
+      {
+        uint32_t raw[128];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_ld32(t_s + 32 * q, *reinterpret_cast<uint32_t(*)[32]>(raw + 32 * q));
+        tc_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 128; ++j) v[j] = __uint_as_float(raw[j]);
+      }
+      const int left = lim - t * 128;
+      if (__any_sync(0xffffffffu, left < 128) || gone) {
+#pragma unroll
+        for (int j = 0; j < 128; ++j) v[j] = (j < left && !((gone >> (j >> 4)) & 1u)) ? v[j] : -INFINITY;
+      }
+      float a0 = fmax3(v[0], v[1], v[2]), a1 = fmax3(v[3], v[4], v[5]), a2 = fmaxf(v[6], v[7]), a3 = fmaxf(v[8], v[9]);
+#pragma unroll
+      for (int j = 10; j < 122; j += 8) {
+        a0 = fmax3(a0, v[j], v[j + 1]);
+        a1 = fmax3(a1, v[j + 2], v[j + 3]);
+        a2 = fmax3(a2, v[j + 4], v[j + 5]);
+        a3 = fmax3(a3, v[j + 6], v[j + 7]);
+      }
+      a0 = fmax3(a0, v[122], v[123]);
+      a1 = fmax3(a1, v[124], v[125]);
+      a2 = fmax3(a2, v[126], v[127]);
+      const float top = fmaxf(fmax3(a0, a1, a2), a3) * c;
+      const bool up = top > m + 8.f;
+      if (__any_sync(0xffffffffu, up)) {
+        const float mn = up ? top : m;
+        const float mun = mn == -INFINITY ? 0.f : mn;
+        const float alpha = m == -INFINITY ? 0.f : ex2(m - mun);
+        l0 *= alpha;
+        l1 *= alpha;
+        if (t > 0) {                       // P V(t - 1) is complete: S(t) was issued after it
+#pragma unroll
+          for (int q = 0; q < D / 32; ++q) {
+            uint32_t o[32];
+            tmem_ld32(t_o + 32 * q, o);
+            tc_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+            tmem_st32(t_o + 32 * q, o);
+          }
+        }
+        m = mn;
+        mu = mun;
+      }
+      uint32_t pk[2][32];
+#pragma unroll
+      for (int j = 0; j < 128; j += 2) {
+        float e0, e1;
+        ffma2_bc(e0, e1, v[j], v[j + 1], c, -mu);
+        e0 = ex2(e0);
+        e1 = ex2(e1);
+        fadd2(l0, l1, l0, l1, e0, e1);
+        pk[j >> 6][(j >> 1) & 31] = pack_bf162(e0, e1);
+      }
+      tmem_st32(t_s, pk[0]);
+      tmem_st32(t_s + 32, pk[1]);
+      tc_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.bar_p_full[x]);
+    }
+    // ---- out = O / l, or the split's part
+    if (ok && n > 0) ok = warp_wait_tc(&s.bar_pv[x], (n - 1) & 1, abort_flag, p.status, kStatusTimeoutPV | 4 | x);
+    if (ok) {
+      tc_fence_after();
+      const float sum = l0 + l1;
+      const float inv = sum > 0.f ? 1.f / sum : 0.f;
+      const float lse2 = sum > 0.f ? mu + log2f(sum) : -INFINITY;
+      const int64_t orow = static_cast<int64_t>(rq.start + i) * p.Hq + head * G + h;
+#pragma unroll 1
+      for (int q = 0; q < D / 32; ++q) {
+        uint32_t o[32];
+        if (n > 0) {
+          tmem_ld32(t_o + 32 * q, o);
+          tc_wait_ld();
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) o[j] = 0u;
+        }
+        if (live) {
+          // columns 2 j, 2 j + 1 of each 8 hold channels j, j + 4
+          if (used_splits == 1) {
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              float e[8];
+#pragma unroll
+              for (int j = 0; j < 8; ++j) e[(j >> 1) + 4 * (j & 1)] = __uint_as_float(o[8 * w + j]) * inv;
+              *reinterpret_cast<uint4*>(p.out + orow * D + 32 * q + 8 * w) =
+                  make_uint4(pack_bf162(e[0], e[1]), pack_bf162(e[2], e[3]), pack_bf162(e[4], e[5]), pack_bf162(e[6], e[7]));
+            }
+          } else {
+            float* po = sp.part_o + (orow * sp.splits + split) * D + 32 * q;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              float e[8];
+#pragma unroll
+              for (int j = 0; j < 8; ++j) e[(j >> 1) + 4 * (j & 1)] = __uint_as_float(o[8 * w + j]) * inv;
+              *reinterpret_cast<float4*>(po + 8 * w) = make_float4(e[0], e[1], e[2], e[3]);
+              *reinterpret_cast<float4*>(po + 8 * w + 4) = make_float4(e[4], e[5], e[6], e[7]);
+            }
+          }
+        }
+      }
+      if (live) {
+        if (used_splits > 1) sp.part_lse[orow * sp.splits + split] = lse2;
+        else if (p.lse) p.lse[orow] = lse2 * 0.6931471805599453f;
+      }
+    }
+    tc_fence_before();
+  }
+
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTcCols);
+  }
+}
+
+template <int D>
+cudaError_t launch_tc_d(const PagedParams& p, const SplitParams& sp, int64_t units, cudaStream_t stream) {
+  // the softmax warps' registers come from the block's launch allocation: a build with fewer registers
+  // per thread than the split assumes would make them wait forever
+  static int regs = -1;
+  if (regs < 0) {
+    cudaFuncAttributes fa;
+    const cudaError_t e = cudaFuncGetAttributes(&fa, paged_tc_kernel<D>);
+    if (e != cudaSuccess) return e;
+    regs = fa.numRegs;
+  }
+  if (regs != kTcLaunchRegs) return cudaErrorInvalidConfiguration;
+  const int smem = static_cast<int>(sizeof(TcSmem<D>) + 1024);
+  const cudaError_t e = cudaFuncSetAttribute(paged_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  paged_tc_kernel<D><<<static_cast<unsigned>(units), kTcThreads, smem, stream>>>(p, sp);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_paged_tc(const PagedParams& p, const SplitParams& sp, int d, int64_t units, cudaStream_t stream) {
+  // a timeout is reported in the status word, which no CTA can clear for the others
+  const cudaError_t e = cudaMemsetAsync(p.status, 0, sizeof(unsigned int), stream);
+  if (e != cudaSuccess) return e;
+  return d == 128 ? launch_tc_d<128>(p, sp, units, stream) : launch_tc_d<64>(p, sp, units, stream);
+}
+
+}  // namespace mxattn
