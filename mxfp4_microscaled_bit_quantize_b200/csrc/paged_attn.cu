@@ -220,12 +220,11 @@ __global__ void __launch_bounds__(kSmallWarps * 32, NT == 1 ? 4 : 2) paged_small
 
   // one group ahead in registers, its page looked up one group earlier still
   auto page_of = [&](int grp) -> int {
-    if (grp >= stop) return -1;
-    const int pg = __ldg(table + ((grp << 4) >> p.page_shift));
-    return static_cast<uint32_t>(pg) < static_cast<uint64_t>(p.n_pages) ? pg : -1;
+    return grp < stop ? __ldg(table + ((grp << 4) >> p.page_shift)) : -1;     // looked at when it is used: a comparison would wait
   };
+  const uint32_t n_pages = static_cast<uint32_t>(p.n_pages);
   auto fetch = [&](Frag<NB>& f, int grp, int page) {
-    if (page >= 0)
+    if (static_cast<uint32_t>(page) < n_pages)
       load_frag(f, p.cache + (static_cast<int64_t>(page) * p.Hkv + head) * head_bytes, (static_cast<uint32_t>(grp) << 4) & page_mask, p.page_shift, lane);
   };
   int grp = first + static_cast<int>(warp);
@@ -235,7 +234,7 @@ __global__ void __launch_bounds__(kSmallWarps * 32, NT == 1 ? 4 : 2) paged_small
   for (; grp < stop; grp += kSmallWarps) {
     fetch(fn, grp + kSmallWarps, page_next);
     const int page_after = page_of(grp + 2 * kSmallWarps);
-    if (page >= 0) {
+    if (static_cast<uint32_t>(page) < n_pages) {
       const int key0 = grp << 4;
       // ---- S^T: partial scores of each 32-channel block, times the block's scale
       float s[NT][4];

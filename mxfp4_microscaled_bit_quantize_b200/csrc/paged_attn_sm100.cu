@@ -35,16 +35,18 @@ static_assert(kIssueRegs + kConvRegs + 2 * kRowRegs == 4 * kTcLaunchRegs, "regis
 constexpr uint32_t kTcCols = 512, kColSx = 0, kColOx = 256;   // S / P of tile X at 128 X, O at 256 + 128 X
 constexpr uint32_t kSw128 = 2;                                // descriptor code of the 128-byte swizzle
 constexpr int kTcStages = 2;
+constexpr int kTurnAfter = 2;          // quarter of a tile's exponentials after which the other tile may start
 
 template <int D>
 struct __align__(1024) TcSmem {
+  static_assert(D == 64 || D == 128, "Q and the output stage are laid out for these");
   static constexpr int kTile = 128 * D * 2;      // 128 rows of D bf16, as D / 64 slabs of 128 x 128 bytes
-  uint8_t q[2][kTile];
+  uint8_t q[2][32768];                           // the tile's Q, and 128 rows x 256 bytes of output at the end
   uint8_t k[kTcStages][kTile];
   uint8_t v[kTcStages][kTile];
   uint64_t bar_q;
   uint64_t bar_k_full[kTcStages], bar_v_full[kTcStages], bar_k_empty[kTcStages], bar_v_empty[kTcStages];
-  uint64_t bar_s_full[2], bar_p_full[2], bar_pv[2], bar_drain[2];
+  uint64_t bar_s_full[2], bar_p_full[2], bar_pv[2], bar_drain[2], bar_turn[2];
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -77,17 +79,26 @@ __device__ __forceinline__ uint32_t mul_bf162(uint32_t a, uint32_t b) {
   return r;
 }
 
+// 16 consecutive 32-bit TMEM columns of this thread's lane (warp-collective).
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+               "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+               : "memory");
+}
+
 // Eight codes times 2^(s - 127) as bf16, in the order e0 e4 e1 e5 e2 e6 e3 e7. A nibble (s eem) shifted
 // to the sign and to the three bits at the border of bf16's exponent and mantissa is the code's value
 // times 2^-126, exactly (code 1, E2M1's subnormal, becomes a bf16 subnormal), so one product by
 // 2^(s - 1) finishes it; scales above 2 need a second one, since 2^(s - 1) leaves bf16's range there.
+template <bool LARGE>
 __device__ __forceinline__ void codes_to_bf16(uint32_t w, uint32_t s, uint32_t (&r)[4]) {
-  const uint32_t mul = (min(s, 128u) + 126u) * 0x00800080u;
+  const uint32_t mul = ((LARGE ? min(s, 128u) : s) + 126u) * 0x00800080u;
   const uint32_t t[4] = {w << 12, w << 8, w << 4, w};
 #pragma unroll
   for (int j = 0; j < 4; ++j) r[j] = mul_bf162(((t[j] >> 6) & 0x01C001C0u) | (t[j] & 0x80008000u), mul);
-  if (s > 128u) {
-    const uint32_t more = (s - 1u) * 0x00800080u;
+  if (LARGE) {
+    const uint32_t more = (max(s, 128u) - 1u) * 0x00800080u;             // 2^(s - 128), or 1
 #pragma unroll
     for (int j = 0; j < 4; ++j) r[j] = mul_bf162(r[j], more);
   }
@@ -126,8 +137,8 @@ __device__ __forceinline__ void block_words(const uint2& o, uint32_t (&q)[2]) {
 // Rows of a tile into shared memory: 16-byte column j of row r in slab j / 8 at (j % 8) ^ (r % 8).
 // Lanes of odd rows take the blocks of a pair in the other order, so that the eight lanes of a store
 // phase (two rows, four pieces) cover all banks.
-template <int D, int W>
-__device__ __forceinline__ void store_rows(const Raw<D>& raw, uint32_t tile, uint32_t row0, uint32_t lane) {
+template <int D, int W, bool LARGE>
+__device__ __forceinline__ void store_rows_as(const Raw<D>& raw, uint32_t tile, uint32_t row0, uint32_t lane) {
   constexpr int NB = D / 32;
   const uint32_t c = lane & 3u, odd = (lane >> 2) & 1u;
 #pragma unroll
@@ -140,11 +151,20 @@ __device__ __forceinline__ void store_rows(const Raw<D>& raw, uint32_t tile, uin
       const uint32_t bx = static_cast<uint32_t>(b) ^ odd;
       const uint32_t w = odd ? q[b ^ 1] : q[b];
       uint32_t r[4];
-      codes_to_bf16(w, (raw.s[i] >> (8u * bx)) & 0xFFu, r);
+      codes_to_bf16<LARGE>(w, (raw.s[i] >> (8u * bx)) & 0xFFu, r);
       const uint32_t col = 4u * bx + c;
       st_shared_v4(tile + (col >> 3) * (128u * 128u) + row * 128u + (((col ^ row) & 7u) << 4), r[0], r[1], r[2], r[3]);
     }
   }
+}
+
+// One choice for the warp's rows: any scale byte of 128 or more takes the form with two products.
+template <int D, int W>
+__device__ __forceinline__ void store_rows(const Raw<D>& raw, uint32_t tile, uint32_t row0, uint32_t lane) {
+  if (__any_sync(0xffffffffu, ((raw.s[0] | raw.s[1] | raw.s[2] | raw.s[3]) & 0x80808080u) != 0u))
+    store_rows_as<D, W, true>(raw, tile, row0, lane);
+  else
+    store_rows_as<D, W, false>(raw, tile, row0, lane);
 }
 
 template <int D>
@@ -196,6 +216,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const PagedPara
       mbar_init(&s.bar_s_full[x], 1);
       mbar_init(&s.bar_p_full[x], 4);
       mbar_init(&s.bar_pv[x], 1);
+      mbar_init(&s.bar_turn[x], 4);
       mbar_init(&s.bar_drain[x], 1);
     }
     s.abort_flag = 0;
@@ -272,22 +293,20 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const PagedPara
     regs_dec<kConvRegs>();
     // ======================= conversion: pages -> bf16 tiles =======================
     const uint32_t row0 = static_cast<uint32_t>(warp - 4) * 32u, g8 = static_cast<uint32_t>(lane) >> 2, c = lane & 3;
-    const uint32_t shift = p.page_shift, page_mask = (1u << shift) - 1u;
+    const uint32_t shift = p.page_shift, page_mask = (1u << shift) - 1u, n_pages = static_cast<uint32_t>(p.n_pages);
     const uint32_t codes = static_cast<uint32_t>(D / 2) << shift;         // bytes of codes in a chunk
     const uint32_t chunk = codes + (static_cast<uint32_t>(NB) << shift);
     const uint64_t page_stride = static_cast<uint64_t>(p.Hkv) * 2u * chunk;
     const uint8_t* base = p.cache + static_cast<uint64_t>(head) * 2u * chunk;
     const int32_t* table = p.block_table + static_cast<int64_t>(r) * p.table_width;
-    // pages of this warp's two groups of 16 keys in tile t (-1: none)
+    // table entries of this warp's two groups of 16 keys in tile t (-1: none). They are looked at when
+    // the codes are loaded, a tile later: a comparison here would wait for them.
     auto pages_of = [&](int t, int (&pg)[2]) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int64_t key = key_begin + t * 128ll + row0 + 16 * j;
         pg[j] = -1;
-        if (t < n_max && key < lim_all) {
-          const int v = __ldg(table + (key >> shift));
-          if (v >= 0 && v < p.n_pages) pg[j] = v;
-        }
+        if (t < n_max && key < lim_all) pg[j] = __ldg(table + (key >> shift));
       }
     };
     auto load = [&](Raw<D>& raw, int t, const int (&pg)[2], int which) {
@@ -296,7 +315,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const PagedPara
         const int64_t key = key_begin + t * 128ll + row0 + 8 * i + g8;
         clear(raw.w[i]);
         raw.s[i] = 0;
-        if (pg[i >> 1] >= 0 && key < lim_all) {
+        if (static_cast<uint32_t>(pg[i >> 1]) < n_pages && key < lim_all) {
           const uint32_t off = static_cast<uint32_t>(key) & page_mask, o16 = off & ~15u;
           const uint8_t* ch = base + static_cast<uint32_t>(pg[i >> 1]) * page_stride + which * chunk;
           load_piece(raw.w[i], ch + off * (D / 2) + c * (D / 8));
@@ -344,18 +363,21 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const PagedPara
     const int row = pair * 256 + x * 128 + in_tile;
     const int i = row / G, h = row - i * G;
     const bool live = row < rows_all;
-    const int n = x == 0 ? n_x[0] : n_x[1];
+    const int n = x == 0 ? n_x[0] : n_x[1], n_other = x == 0 ? n_x[1] : n_x[0];
     // Q row into shared memory, each 8 channels in the order of the converted codes
     if (n > 0) {
       const __nv_bfloat16* src = p.q + (rq.start + (live ? i : 0)) * p.q_token_stride + (head * G + h) * p.q_head_stride;
       const uint32_t tile = smem_u32(s.q[x]);
+      uint4 w[D / 8];                       // all loads in flight before the first store
 #pragma unroll
       for (int j = 0; j < D / 8; ++j) {
-        uint4 w = make_uint4(0u, 0u, 0u, 0u);
-        if (live) w = *reinterpret_cast<const uint4*>(src + j * 8);
-        st_shared_v4(tile + (j >> 3) * (128u * 128u) + in_tile * 128u + (((j ^ in_tile) & 7) << 4), lo16x2(w.x, w.z), hi16x2(w.x, w.z), lo16x2(w.y, w.w),
-                     hi16x2(w.y, w.w));
+        w[j] = make_uint4(0u, 0u, 0u, 0u);
+        if (live) w[j] = *reinterpret_cast<const uint4*>(src + j * 8);
       }
+#pragma unroll
+      for (int j = 0; j < D / 8; ++j)
+        st_shared_v4(tile + (j >> 3) * (128u * 128u) + in_tile * 128u + (((j ^ in_tile) & 7) << 4), lo16x2(w[j].x, w[j].z), hi16x2(w[j].x, w[j].z),
+                     lo16x2(w[j].y, w[j].w), hi16x2(w[j].y, w[j].w));
       fence_proxy_async_smem();
     }
     __syncwarp();
@@ -367,20 +389,22 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const PagedPara
     const int lim = live ? static_cast<int>(max(limit_of(row) - key_begin, static_cast<int64_t>(0))) : 0;   // in the split
     const uint32_t shift = p.page_shift;
     const int32_t* table = p.block_table + static_cast<int64_t>(r) * p.table_width;
-    // lane j < 8 looks after keys 16 j .. 16 j + 15 of a tile: is their page there?
-    auto missing = [&](int t) -> bool {
+    // lane j < 8 looks after keys 16 j .. 16 j + 15 of a tile: their table entry, one tile ahead
+    const uint32_t n_pages = static_cast<uint32_t>(p.n_pages);
+    auto entry_of = [&](int t) -> int {
       const int64_t key = key_begin + t * 128ll + lane * 16;
-      if (t >= n || lane >= 8 || key >= lim_all) return false;
-      const int v = __ldg(table + (key >> shift));
-      return v < 0 || v >= p.n_pages;
+      return t < n && lane < 8 && key < lim_all ? __ldg(table + (key >> shift)) : 0;
     };
     float m = -INFINITY, mu = 0.f, l0 = 0.f, l1 = 0.f;
-    bool miss = missing(0);
+    int entry = entry_of(0);
     bool ok = true;
     for (int t = 0; ok && t < n; ++t) {
-      const uint32_t gone = __ballot_sync(0xffffffffu, miss);
-      miss = missing(t + 1);
+      const uint32_t gone = __ballot_sync(0xffffffffu, static_cast<uint32_t>(entry) >= n_pages && lane < 8 && key_begin + t * 128ll + lane * 16 < lim_all);
+      entry = entry_of(t + 1);
       ok = warp_wait_tc(&s.bar_s_full[x], t & 1, abort_flag, p.status, kStatusTimeoutS | x);
+      // the tiles' exponentials take turns, so that one tile's products run under the other's softmax
+      const int before = x == 0 ? t - 1 : t;
+      if (ok && before >= 0 && before < n_other) ok = warp_wait_tc(&s.bar_turn[x], before & 1, abort_flag, p.status, kStatusTimeoutS | 4 | x);
       if (!ok) break;
       tc_fence_after();
       float v[128];
@@ -430,18 +454,21 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const PagedPara
         m = mn;
         mu = mun;
       }
-      uint32_t pk[2][32];
 #pragma unroll
-      for (int j = 0; j < 128; j += 2) {
-        float e0, e1;
-        ffma2_bc(e0, e1, v[j], v[j + 1], c, -mu);
-        e0 = ex2(e0);
-        e1 = ex2(e1);
-        fadd2(l0, l1, l0, l1, e0, e1);
-        pk[j >> 6][(j >> 1) & 31] = pack_bf162(e0, e1);
+      for (int q = 0; q < 4; ++q) {        // 32 scores become 16 columns of P, over S columns that are in registers
+        uint32_t pk[16];
+#pragma unroll
+        for (int j = 0; j < 32; j += 2) {
+          float e0, e1;
+          ffma2_bc(e0, e1, v[32 * q + j], v[32 * q + j + 1], c, -mu);
+          e0 = ex2(e0);
+          e1 = ex2(e1);
+          fadd2(l0, l1, l0, l1, e0, e1);
+          pk[j >> 1] = pack_bf162(e0, e1);
+        }
+        tmem_st16(t_s + 16 * q, pk);
+        if (q == kTurnAfter && lane == 0) mbar_arrive(&s.bar_turn[x ^ 1]);
       }
-      tmem_st32(t_s, pk[0]);
-      tmem_st32(t_s + 32, pk[1]);
       tc_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -455,6 +482,24 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const PagedPara
       const float inv = sum > 0.f ? 1.f / sum : 0.f;
       const float lse2 = sum > 0.f ? mu + log2f(sum) : -INFINITY;
       const int64_t orow = static_cast<int64_t>(rq.start + i) * p.Hq + head * G + h;
+      const uint32_t live_rows = __popc(__ballot_sync(0xffffffffu, live));    // the warp's first rows
+      // The rows leave through shared memory (Q's, which no product reads any more), so that a store
+      // instruction covers whole lines: passes of up to 256 bytes of each of the warp's 32 rows, piece j
+      // of row rr at j ^ (rr % 8). Columns 2 j, 2 j + 1 of each 8 hold channels j, j + 4.
+      const uint32_t stage = smem_u32(s.q[x]) + static_cast<uint32_t>(quarter) * 8192u;
+      const uint32_t my_row = stage + static_cast<uint32_t>(lane) * 256u, sw = static_cast<uint32_t>(lane) & 7u;
+      auto put = [&](uint32_t piece, uint32_t a, uint32_t b, uint32_t cc, uint32_t d) { st_shared_v4(my_row + ((piece ^ sw) << 4), a, b, cc, d); };
+      auto flush = [&](uint32_t pieces, uint8_t* dst, int64_t row_bytes) {    // pieces of 16 bytes per row: 8 or 16
+        __syncwarp();
+        const uint32_t per = 32u / pieces, pc = static_cast<uint32_t>(lane) % pieces;
+        for (uint32_t r0 = 0; r0 < live_rows; r0 += per) {
+          const uint32_t rr = r0 + static_cast<uint32_t>(lane) / pieces;
+          const int64_t to = __shfl_sync(0xffffffffu, orow, rr & 31u);
+          if (rr < live_rows) *reinterpret_cast<uint4*>(dst + to * row_bytes + pc * 16u) = ld_shared_v4(stage + rr * 256u + ((pc ^ (rr & 7u)) << 4));
+        }
+        __syncwarp();
+      };
+      const bool direct = used_splits == 1;
 #pragma unroll 1
       for (int q = 0; q < D / 32; ++q) {
         uint32_t o[32];
@@ -465,30 +510,22 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const PagedPara
 #pragma unroll
           for (int j = 0; j < 32; ++j) o[j] = 0u;
         }
-        if (live) {
-          // columns 2 j, 2 j + 1 of each 8 hold channels j, j + 4
-          if (used_splits == 1) {
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              float e[8];
+        for (int w = 0; w < 4; ++w) {
+          float e[8];
 #pragma unroll
-              for (int j = 0; j < 8; ++j) e[(j >> 1) + 4 * (j & 1)] = __uint_as_float(o[8 * w + j]) * inv;
-              *reinterpret_cast<uint4*>(p.out + orow * D + 32 * q + 8 * w) =
-                  make_uint4(pack_bf162(e[0], e[1]), pack_bf162(e[2], e[3]), pack_bf162(e[4], e[5]), pack_bf162(e[6], e[7]));
-            }
+          for (int j = 0; j < 8; ++j) e[(j >> 1) + 4 * (j & 1)] = __uint_as_float(o[8 * w + j]) * inv;
+          if (direct) {
+            put(4 * q + w, pack_bf162(e[0], e[1]), pack_bf162(e[2], e[3]), pack_bf162(e[4], e[5]), pack_bf162(e[6], e[7]));
           } else {
-            float* po = sp.part_o + (orow * sp.splits + split) * D + 32 * q;
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              float e[8];
-#pragma unroll
-              for (int j = 0; j < 8; ++j) e[(j >> 1) + 4 * (j & 1)] = __uint_as_float(o[8 * w + j]) * inv;
-              *reinterpret_cast<float4*>(po + 8 * w) = make_float4(e[0], e[1], e[2], e[3]);
-              *reinterpret_cast<float4*>(po + 8 * w + 4) = make_float4(e[4], e[5], e[6], e[7]);
-            }
+            put(8 * (q & 1) + 2 * w, __float_as_uint(e[0]), __float_as_uint(e[1]), __float_as_uint(e[2]), __float_as_uint(e[3]));
+            put(8 * (q & 1) + 2 * w + 1, __float_as_uint(e[4]), __float_as_uint(e[5]), __float_as_uint(e[6]), __float_as_uint(e[7]));
           }
         }
+        if (!direct && (q & 1))
+          flush(16, reinterpret_cast<uint8_t*>(sp.part_o + static_cast<int64_t>(split) * D + 32 * (q - 1)), static_cast<int64_t>(sp.splits) * D * 4);
       }
+      if (direct) flush(D / 8, reinterpret_cast<uint8_t*>(p.out), D * 2);
       if (live) {
         if (used_splits > 1) sp.part_lse[orow * sp.splits + split] = lse2;
         else if (p.lse) p.lse[orow] = lse2 * 0.6931471805599453f;
