@@ -29,13 +29,13 @@ namespace mxattn {
 
 namespace {
 
-constexpr int kTcThreads = 512, kTcLaunchRegs = 128;
-constexpr int kIssueRegs = 56, kConvRegs = 88, kRowRegs = 184;
-static_assert(kIssueRegs + kConvRegs + 2 * kRowRegs == 4 * kTcLaunchRegs, "register split");
+constexpr int kTcThreads = 896, kTcLaunchRegs = 72;
+constexpr int kIssueRegs = 40, kConvRegs = 56, kRowRegs = 88;
+static_assert(kIssueRegs + 2 * kConvRegs + 4 * kRowRegs <= 7 * kTcLaunchRegs, "register split");
+constexpr int kConvWarp0 = 4, kRowWarp0 = 12;    // warps 0-3 issue, 4-11 convert, 12-27 softmax
 constexpr uint32_t kTcCols = 512, kColSx = 0, kColOx = 256;   // S / P of tile X at 128 X, O at 256 + 128 X
 constexpr uint32_t kSw128 = 2;                                // descriptor code of the 128-byte swizzle
 constexpr int kTcStages = 2;
-constexpr int kTurnAfter = 2;          // quarter of a tile's exponentials after which the other tile may start
 
 template <int D>
 struct __align__(1024) TcSmem {
@@ -64,8 +64,24 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, ui
                "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
 }
 
+// mbar_wait whose loop is a bare try_wait: the abort flag and the clock are looked at every 64th time,
+// since the instructions of the waiting warps are taken from the working ones.
+__device__ __forceinline__ bool mbar_poll(uint64_t* bar, uint32_t parity, volatile int* abort_flag, unsigned int* status, unsigned int code) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  for (;;) {
+    for (int i = 0; i < 64; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+    if (*abort_flag) return false;
+    if (global_timer_ns() - t0 > kWaitTimeoutNs) {
+      *abort_flag = 1;
+      atomicCAS(status, 0u, code);
+      return false;
+    }
+  }
+}
 __device__ __forceinline__ bool warp_wait_tc(uint64_t* bar, uint32_t parity, volatile int* abort_flag, unsigned int* status, unsigned int code) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status, code));
+  return __all_sync(0xffffffffu, mbar_poll(bar, parity, abort_flag, status, code));
 }
 __device__ __forceinline__ void drain_wait_tc(uint64_t* bar, uint32_t parity) {
   const uint64_t t0 = global_timer_ns();
@@ -79,11 +95,16 @@ __device__ __forceinline__ uint32_t mul_bf162(uint32_t a, uint32_t b) {
   return r;
 }
 
-// 16 consecutive 32-bit TMEM columns of this thread's lane (warp-collective).
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
-               "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+// 16 TMEM lanes, two halves of the warp, the upper one kOff columns on: 16 columns each.
+template <int kOff>
+__device__ __forceinline__ void tmem_ld16x2_16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x32bx2.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16], %17;"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+               : "r"(taddr), "n"(kOff));
+}
+template <int kOff>
+__device__ __forceinline__ void tmem_st16x2_16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile("tcgen05.st.sync.aligned.16x32bx2.x16.b32 [%0], %1, {%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17};" ::"r"(taddr), "n"(kOff), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
                : "memory");
 }
 
@@ -104,11 +125,11 @@ __device__ __forceinline__ void codes_to_bf16(uint32_t w, uint32_t s, uint32_t (
   }
 }
 
-// What a converting lane holds of a tile's K or V: piece (lane & 3) of rows (lane >> 2) + 8 i of its
-// warp's 32, and those rows' scale bytes.
+// What a converting lane holds of a tile's K or V: piece (lane & 3) of rows (lane >> 2) and
+// (lane >> 2) + 8 of its warp's 16, and those rows' scale bytes.
 template <int D> struct Raw;
-template <> struct Raw<128> { uint4 w[4]; uint32_t s[4]; };
-template <> struct Raw<64> { uint2 w[4]; uint32_t s[4]; };
+template <> struct Raw<128> { uint4 w[2]; uint32_t s[2]; };
+template <> struct Raw<64> { uint2 w[2]; uint32_t s[2]; };
 
 __device__ __forceinline__ void clear(uint4& v) { v = make_uint4(0u, 0u, 0u, 0u); }
 __device__ __forceinline__ void clear(uint2& v) { v = make_uint2(0u, 0u); }
@@ -142,7 +163,7 @@ __device__ __forceinline__ void store_rows_as(const Raw<D>& raw, uint32_t tile, 
   constexpr int NB = D / 32;
   const uint32_t c = lane & 3u, odd = (lane >> 2) & 1u;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 2; ++i) {
     const uint32_t row = row0 + 8u * i + (lane >> 2);
     uint32_t q[NB];
     block_words<W>(raw.w[i], q);
@@ -161,7 +182,7 @@ __device__ __forceinline__ void store_rows_as(const Raw<D>& raw, uint32_t tile, 
 // One choice for the warp's rows: any scale byte of 128 or more takes the form with two products.
 template <int D, int W>
 __device__ __forceinline__ void store_rows(const Raw<D>& raw, uint32_t tile, uint32_t row0, uint32_t lane) {
-  if (__any_sync(0xffffffffu, ((raw.s[0] | raw.s[1] | raw.s[2] | raw.s[3]) & 0x80808080u) != 0u))
+  if (__any_sync(0xffffffffu, ((raw.s[0] | raw.s[1]) & 0x80808080u) != 0u))
     store_rows_as<D, W, true>(raw, tile, row0, lane);
   else
     store_rows_as<D, W, false>(raw, tile, row0, lane);
@@ -173,7 +194,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const PagedPara
   using Sm = TcSmem<D>;
   extern __shared__ uint8_t smem_raw[];
   Sm& s = *reinterpret_cast<Sm*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;   // uniform: descriptors in uniform registers
 
   // ---- work unit
   const int G = p.Hq / p.Hkv;
@@ -205,18 +226,18 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const PagedPara
   const int n_max = max(n_x[0], n_x[1]);
 
   if (threadIdx.x == 0) {
-    mbar_init(&s.bar_q, 8);
+    mbar_init(&s.bar_q, 16);
     for (int i = 0; i < kTcStages; ++i) {
-      mbar_init(&s.bar_k_full[i], 4);
-      mbar_init(&s.bar_v_full[i], 4);
+      mbar_init(&s.bar_k_full[i], 8);
+      mbar_init(&s.bar_v_full[i], 8);
       mbar_init(&s.bar_k_empty[i], 2);
       mbar_init(&s.bar_v_empty[i], 2);
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(&s.bar_s_full[x], 1);
-      mbar_init(&s.bar_p_full[x], 4);
+      mbar_init(&s.bar_p_full[x], 8);
       mbar_init(&s.bar_pv[x], 1);
-      mbar_init(&s.bar_turn[x], 4);
+      mbar_init(&s.bar_turn[x], 8);
       mbar_init(&s.bar_drain[x], 1);
     }
     s.abort_flag = 0;
@@ -244,9 +265,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const PagedPara
       const uint32_t a_q = smem_u32(s.q[x]) >> 4, a_k = smem_u32(s.k[0]) >> 4, a_v = smem_u32(s.v[0]) >> 4;
       const uint32_t t_s = tmem + kColSx + 128 * x, t_o = tmem + kColOx + 128 * x;
       bool ok = n_own == 0 || warp_wait_tc(&s.bar_q, 0, abort_flag, p.status, kStatusTimeoutQ);
-      auto issue_s = [&](int t) -> bool {
+      auto wait_k = [&](int t) -> bool {
+        return warp_wait_tc(&s.bar_k_full[t % kTcStages], (t / kTcStages) & 1, abort_flag, p.status, kStatusTimeoutKV | (t % kTcStages));
+      };
+      auto issue_s = [&](int t) {
         const int st = t % kTcStages;
-        if (!warp_wait_tc(&s.bar_k_full[st], (t / kTcStages) & 1, abort_flag, p.status, kStatusTimeoutKV | st)) return false;
         tc_fence_after();
         if (leader) {
 #pragma unroll
@@ -259,13 +282,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const PagedPara
           if (t >= n_other) mbar_arrive(&s.bar_k_empty[st]);               // the other tile has no product here
         }
         __syncwarp();
-        return true;
       };
-      if (ok && n_own > 0) ok = issue_s(0);
+      if (ok && n_own > 0) {
+        ok = wait_k(0);
+        if (ok) issue_s(0);
+      }
       for (int t = 0; ok && t < n_own; ++t) {
         const int st = t % kTcStages;
-        ok = warp_wait_tc(&s.bar_p_full[x], t & 1, abort_flag, p.status, kStatusTimeoutP | x) &&
-             warp_wait_tc(&s.bar_v_full[st], (t / kTcStages) & 1, abort_flag, p.status, kStatusTimeoutKV | 8 | st);
+        ok = warp_wait_tc(&s.bar_v_full[st], (t / kTcStages) & 1, abort_flag, p.status, kStatusTimeoutKV | 8 | st) &&
+             warp_wait_tc(&s.bar_p_full[x], t & 1, abort_flag, p.status, kStatusTimeoutP | x);
         if (!ok) break;
         tc_fence_after();
         if (leader) {
@@ -279,7 +304,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const PagedPara
         __syncwarp();
         if (t + 1 < n_own) {
           // S(t + 1) overwrites the columns that hold P(t)
-          ok = warp_wait_tc(&s.bar_pv[x], t & 1, abort_flag, p.status, kStatusTimeoutPV | x) && issue_s(t + 1);
+          ok = wait_k(t + 1) && warp_wait_tc(&s.bar_pv[x], t & 1, abort_flag, p.status, kStatusTimeoutPV | x);
+          if (ok) issue_s(t + 1);
         }
       }
       // everything issued above must complete before TMEM is released
@@ -289,45 +315,40 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const PagedPara
       }
       __syncwarp();
     }
-  } else if (warp < 8) {
+  } else if (warp < kRowWarp0) {
     regs_dec<kConvRegs>();
     // ======================= conversion: pages -> bf16 tiles =======================
-    const uint32_t row0 = static_cast<uint32_t>(warp - 4) * 32u, g8 = static_cast<uint32_t>(lane) >> 2, c = lane & 3;
+    const uint32_t row0 = static_cast<uint32_t>(warp - kConvWarp0) * 16u, g8 = static_cast<uint32_t>(lane) >> 2, c = lane & 3;
     const uint32_t shift = p.page_shift, page_mask = (1u << shift) - 1u, n_pages = static_cast<uint32_t>(p.n_pages);
     const uint32_t codes = static_cast<uint32_t>(D / 2) << shift;         // bytes of codes in a chunk
     const uint32_t chunk = codes + (static_cast<uint32_t>(NB) << shift);
     const uint64_t page_stride = static_cast<uint64_t>(p.Hkv) * 2u * chunk;
     const uint8_t* base = p.cache + static_cast<uint64_t>(head) * 2u * chunk;
     const int32_t* table = p.block_table + static_cast<int64_t>(r) * p.table_width;
-    // table entries of this warp's two groups of 16 keys in tile t (-1: none). They are looked at when
-    // the codes are loaded, a tile later: a comparison here would wait for them.
-    auto pages_of = [&](int t, int (&pg)[2]) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int64_t key = key_begin + t * 128ll + row0 + 16 * j;
-        pg[j] = -1;
-        if (t < n_max && key < lim_all) pg[j] = __ldg(table + (key >> shift));
-      }
+    // table entry of this warp's 16 keys in tile t (-1: none). It is looked at when the codes are loaded,
+    // a tile later: a comparison here would wait for it.
+    auto page_of = [&](int t) -> int {
+      const int64_t key = key_begin + t * 128ll + row0;
+      return t < n_max && key < lim_all ? __ldg(table + (key >> shift)) : -1;
     };
-    auto load = [&](Raw<D>& raw, int t, const int (&pg)[2], int which) {
+    const uint32_t lane_code = c * (D / 8) + g8 * (D / 2);
+    auto load = [&](Raw<D>& raw, int t, int pg, int which) {
+      const int64_t key0 = key_begin + t * 128ll + row0;
+      const bool there = static_cast<uint32_t>(pg) < n_pages;
+      const uint32_t off = static_cast<uint32_t>(key0) & page_mask;
+      const uint8_t* ch = base + static_cast<uint32_t>(pg) * page_stride + (which ? chunk : 0u);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int64_t key = key_begin + t * 128ll + row0 + 8 * i + g8;
+      for (int i = 0; i < 2; ++i) {
         clear(raw.w[i]);
         raw.s[i] = 0;
-        if (static_cast<uint32_t>(pg[i >> 1]) < n_pages && key < lim_all) {
-          const uint32_t off = static_cast<uint32_t>(key) & page_mask, o16 = off & ~15u;
-          const uint8_t* ch = base + static_cast<uint32_t>(pg[i >> 1]) * page_stride + which * chunk;
-          load_piece(raw.w[i], ch + off * (D / 2) + c * (D / 8));
-          const uint32_t i16 = g8 + 8u * (i & 1);
-          raw.s[i] = load_scales<D>(ch + codes + (o16 + (which ? v_scale_row(i16) : k_scale_row(i16))) * NB);
+        if (there && key0 + 8 * i + g8 < lim_all) {
+          load_piece(raw.w[i], ch + off * (D / 2) + 8 * i * (D / 2) + lane_code);
+          raw.s[i] = load_scales<D>(ch + codes + (off + (which ? v_scale_row(g8 + 8 * i) : k_scale_row(g8 + 8 * i))) * NB);
         }
       }
     };
     Raw<D> rk, rv;
-    int pg[2], pg_next[2];
-    pages_of(0, pg);
-    pages_of(1, pg_next);
+    int pg = page_of(0), pg_next = page_of(1);
     if (n_max > 0) {
       load(rk, 0, pg, 0);
       load(rv, 0, pg, 1);
@@ -336,8 +357,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const PagedPara
     for (int t = 0; ok && t < n_max; ++t) {
       const int st = t % kTcStages;
       const uint32_t par = ((t / kTcStages) & 1) ^ 1;
-      int pg_after[2];
-      pages_of(t + 2, pg_after);
+      const int pg_after = page_of(t + 2);
       if (t >= kTcStages) ok = warp_wait_tc(&s.bar_k_empty[st], par, abort_flag, p.status, kStatusTimeoutEmpty | st);
       if (!ok) break;
       store_rows<D, 0>(rk, smem_u32(s.k[st]), row0, lane);
@@ -352,14 +372,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const PagedPara
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.bar_v_full[st]);
       if (t + 1 < n_max) load(rv, t + 1, pg_next, 1);
-      pg_next[0] = pg_after[0];
-      pg_next[1] = pg_after[1];
+      pg_next = pg_after;
     }
   } else {
     regs_inc<kRowRegs>();
-    // ======================= softmax: one thread per row =======================
-    const int x = (warp - 8) >> 2, quarter = warp & 3;
-    const int in_tile = quarter * 32 + lane;
+    // ======================= softmax: two threads per row =======================
+    // A warp owns 16 rows of its lane quarter; lanes 0-15 take keys 0 .. 63 of a tile, lanes 16-31 keys
+    // 64 .. 127 of the same rows (tcgen05.ld 16x32bx2), and of O the two halves of the channels.
+    const int sw = warp - kRowWarp0, x = sw >> 3, quarter = warp & 3, kh = lane >> 4;
+    const int r0 = quarter * 32 + ((sw >> 2) & 1) * 16;
+    const int in_tile = r0 + (lane & 15);
     const int row = pair * 256 + x * 128 + in_tile;
     const int i = row / G, h = row - i * G;
     const bool live = row < rows_all;
@@ -368,22 +390,24 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const PagedPara
     if (n > 0) {
       const __nv_bfloat16* src = p.q + (rq.start + (live ? i : 0)) * p.q_token_stride + (head * G + h) * p.q_head_stride;
       const uint32_t tile = smem_u32(s.q[x]);
-      uint4 w[D / 8];                       // all loads in flight before the first store
+      uint4 w[D / 16];                      // all loads in flight before the first store
 #pragma unroll
-      for (int j = 0; j < D / 8; ++j) {
+      for (int j = 0; j < D / 16; ++j) {
         w[j] = make_uint4(0u, 0u, 0u, 0u);
-        if (live) w[j] = *reinterpret_cast<const uint4*>(src + j * 8);
+        if (live) w[j] = *reinterpret_cast<const uint4*>(src + (kh * (D / 16) + j) * 8);
       }
 #pragma unroll
-      for (int j = 0; j < D / 8; ++j)
-        st_shared_v4(tile + (j >> 3) * (128u * 128u) + in_tile * 128u + (((j ^ in_tile) & 7) << 4), lo16x2(w[j].x, w[j].z), hi16x2(w[j].x, w[j].z),
-                     lo16x2(w[j].y, w[j].w), hi16x2(w[j].y, w[j].w));
+      for (int jj = 0; jj < D / 16; ++jj) {
+        const int j = kh * (D / 16) + jj;
+        st_shared_v4(tile + (j >> 3) * (128u * 128u) + in_tile * 128u + (((j ^ in_tile) & 7) << 4), lo16x2(w[jj].x, w[jj].z), hi16x2(w[jj].x, w[jj].z),
+                     lo16x2(w[jj].y, w[jj].w), hi16x2(w[jj].y, w[jj].w));
+      }
       fence_proxy_async_smem();
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&s.bar_q);
 
-    const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t lane_addr = static_cast<uint32_t>(r0) << 16;
     const uint32_t t_s = tmem + lane_addr + kColSx + 128 * x, t_o = tmem + lane_addr + kColOx + 128 * x;
     const float c = p.scale_log2;
     const int lim = live ? static_cast<int>(max(limit_of(row) - key_begin, static_cast<int64_t>(0))) : 0;   // in the split
@@ -407,32 +431,34 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const PagedPara
       if (ok && before >= 0 && before < n_other) ok = warp_wait_tc(&s.bar_turn[x], before & 1, abort_flag, p.status, kStatusTimeoutS | 4 | x);
       if (!ok) break;
       tc_fence_after();
-      float v[128];
+      float v[64];                         // keys 64 kh .. of the tile
       {
-        uint32_t raw[128];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) tmem_ld32(t_s + 32 * q, *reinterpret_cast<uint32_t(*)[32]>(raw + 32 * q));
+        uint32_t raw[64];
+        tmem_ld16x2_32<64>(t_s, *reinterpret_cast<uint32_t(*)[32]>(raw));
+        tmem_ld16x2_32<64>(t_s + 32, *reinterpret_cast<uint32_t(*)[32]>(raw + 32));
         tc_wait_ld();
 #pragma unroll
-        for (int j = 0; j < 128; ++j) v[j] = __uint_as_float(raw[j]);
+        for (int j = 0; j < 64; ++j) v[j] = __uint_as_float(raw[j]);
       }
-      const int left = lim - t * 128;
-      if (__any_sync(0xffffffffu, left < 128) || gone) {
+      const int left = lim - t * 128 - 64 * kh;
+      if (__any_sync(0xffffffffu, left < 64) || gone) {
+        const uint32_t gone_h = gone >> (4 * kh);
 #pragma unroll
-        for (int j = 0; j < 128; ++j) v[j] = (j < left && !((gone >> (j >> 4)) & 1u)) ? v[j] : -INFINITY;
+        for (int j = 0; j < 64; ++j) v[j] = (j < left && !((gone_h >> (j >> 4)) & 1u)) ? v[j] : -INFINITY;
       }
       float a0 = fmax3(v[0], v[1], v[2]), a1 = fmax3(v[3], v[4], v[5]), a2 = fmaxf(v[6], v[7]), a3 = fmaxf(v[8], v[9]);
 #pragma unroll
-      for (int j = 10; j < 122; j += 8) {
+      for (int j = 10; j < 58; j += 8) {
         a0 = fmax3(a0, v[j], v[j + 1]);
         a1 = fmax3(a1, v[j + 2], v[j + 3]);
         a2 = fmax3(a2, v[j + 4], v[j + 5]);
         a3 = fmax3(a3, v[j + 6], v[j + 7]);
       }
-      a0 = fmax3(a0, v[122], v[123]);
-      a1 = fmax3(a1, v[124], v[125]);
-      a2 = fmax3(a2, v[126], v[127]);
-      const float top = fmaxf(fmax3(a0, a1, a2), a3) * c;
+      a0 = fmax3(a0, v[58], v[59]);
+      a1 = fmax3(a1, v[60], v[61]);
+      a2 = fmax3(a2, v[62], v[63]);
+      float top = fmaxf(fmax3(a0, a1, a2), a3);
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16)) * c;
       const bool up = top > m + 8.f;
       if (__any_sync(0xffffffffu, up)) {
         const float mn = up ? top : m;
@@ -443,19 +469,19 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const PagedPara
         if (t > 0) {                       // P V(t - 1) is complete: S(t) was issued after it
 #pragma unroll
           for (int q = 0; q < D / 32; ++q) {
-            uint32_t o[32];
-            tmem_ld32(t_o + 32 * q, o);
+            uint32_t o[16];
+            tmem_ld16x2_16<D / 2>(t_o + 16 * q, o);
             tc_wait_ld();
 #pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
-            tmem_st32(t_o + 32 * q, o);
+            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+            tmem_st16x2_16<D / 2>(t_o + 16 * q, o);
           }
         }
         m = mn;
         mu = mun;
       }
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {        // 32 scores become 16 columns of P, over S columns that are in registers
+      for (int q = 0; q < 2; ++q) {        // 32 scores of each half become 16 columns of P, over S columns that are in registers
         uint32_t pk[16];
 #pragma unroll
         for (int j = 0; j < 32; j += 2) {
@@ -466,8 +492,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const PagedPara
           fadd2(l0, l1, l0, l1, e0, e1);
           pk[j >> 1] = pack_bf162(e0, e1);
         }
-        tmem_st16(t_s + 16 * q, pk);
-        if (q == kTurnAfter && lane == 0) mbar_arrive(&s.bar_turn[x ^ 1]);
+        if (q == 1 && lane == 0) mbar_arrive(&s.bar_turn[x ^ 1]);
+        tmem_st16x2_16<32>(t_s + 16 * q, pk);
       }
       tc_wait_st();
       tc_fence_before();
@@ -478,55 +504,64 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const PagedPara
     if (ok && n > 0) ok = warp_wait_tc(&s.bar_pv[x], (n - 1) & 1, abort_flag, p.status, kStatusTimeoutPV | 4 | x);
     if (ok) {
       tc_fence_after();
-      const float sum = l0 + l1;
+      float sum = l0 + l1;
+      sum += __shfl_xor_sync(0xffffffffu, sum, 16);
       const float inv = sum > 0.f ? 1.f / sum : 0.f;
       const float lse2 = sum > 0.f ? mu + log2f(sum) : -INFINITY;
       const int64_t orow = static_cast<int64_t>(rq.start + i) * p.Hq + head * G + h;
-      const uint32_t live_rows = __popc(__ballot_sync(0xffffffffu, live));    // the warp's first rows
+      const uint32_t live_rows = __popc(__ballot_sync(0xffffffffu, live) & 0xFFFFu);   // the warp's first rows
       // The rows leave through shared memory (Q's, which no product reads any more), so that a store
-      // instruction covers whole lines: passes of up to 256 bytes of each of the warp's 32 rows, piece j
+      // instruction covers whole lines: passes of up to 256 bytes of each of the warp's 16 rows, piece j
       // of row rr at j ^ (rr % 8). Columns 2 j, 2 j + 1 of each 8 hold channels j, j + 4.
-      const uint32_t stage = smem_u32(s.q[x]) + static_cast<uint32_t>(quarter) * 8192u;
-      const uint32_t my_row = stage + static_cast<uint32_t>(lane) * 256u, sw = static_cast<uint32_t>(lane) & 7u;
-      auto put = [&](uint32_t piece, uint32_t a, uint32_t b, uint32_t cc, uint32_t d) { st_shared_v4(my_row + ((piece ^ sw) << 4), a, b, cc, d); };
+      const uint32_t stage = smem_u32(s.q[x]) + static_cast<uint32_t>(r0) * 256u;
+      const uint32_t my_row = stage + (lane & 15) * 256u, sw7 = static_cast<uint32_t>(lane) & 7u;
+      auto put = [&](uint32_t piece, uint32_t a, uint32_t b, uint32_t cc, uint32_t d) { st_shared_v4(my_row + ((piece ^ sw7) << 4), a, b, cc, d); };
       auto flush = [&](uint32_t pieces, uint8_t* dst, int64_t row_bytes) {    // pieces of 16 bytes per row: 8 or 16
         __syncwarp();
         const uint32_t per = 32u / pieces, pc = static_cast<uint32_t>(lane) % pieces;
-        for (uint32_t r0 = 0; r0 < live_rows; r0 += per) {
-          const uint32_t rr = r0 + static_cast<uint32_t>(lane) / pieces;
-          const int64_t to = __shfl_sync(0xffffffffu, orow, rr & 31u);
+        for (uint32_t rr0 = 0; rr0 < live_rows; rr0 += per) {
+          const uint32_t rr = rr0 + static_cast<uint32_t>(lane) / pieces;
+          const int64_t to = __shfl_sync(0xffffffffu, orow, rr & 15u);
           if (rr < live_rows) *reinterpret_cast<uint4*>(dst + to * row_bytes + pc * 16u) = ld_shared_v4(stage + rr * 256u + ((pc ^ (rr & 7u)) << 4));
         }
         __syncwarp();
       };
       const bool direct = used_splits == 1;
+      // fp32 parts: 64 channels a pass; with d = 128 a pass takes one half of the lanes' channels
+      const int passes = direct ? 1 : D / 64;
 #pragma unroll 1
-      for (int q = 0; q < D / 32; ++q) {
-        uint32_t o[32];
-        if (n > 0) {
-          tmem_ld32(t_o + 32 * q, o);
-          tc_wait_ld();
-        } else {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) o[j] = 0u;
-        }
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          float e[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) e[(j >> 1) + 4 * (j & 1)] = __uint_as_float(o[8 * w + j]) * inv;
-          if (direct) {
-            put(4 * q + w, pack_bf162(e[0], e[1]), pack_bf162(e[2], e[3]), pack_bf162(e[4], e[5]), pack_bf162(e[6], e[7]));
+      for (int pp = 0; pp < passes; ++pp) {
+#pragma unroll 1
+        for (int q = 0; q < D / 64; ++q) {
+          uint32_t o[32];
+          if (n > 0) {
+            tmem_ld16x2_32<D / 2>(t_o + 32 * q, o);
+            tc_wait_ld();
           } else {
-            put(8 * (q & 1) + 2 * w, __float_as_uint(e[0]), __float_as_uint(e[1]), __float_as_uint(e[2]), __float_as_uint(e[3]));
-            put(8 * (q & 1) + 2 * w + 1, __float_as_uint(e[4]), __float_as_uint(e[5]), __float_as_uint(e[6]), __float_as_uint(e[7]));
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = 0u;
+          }
+          const uint32_t col8 = (kh * (D / 2) + 32 * q) / 8;                  // first of the lane's four groups of 8 channels
+          if (direct || D == 64 || kh == pp) {
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              float e[8];
+#pragma unroll
+              for (int j = 0; j < 8; ++j) e[(j >> 1) + 4 * (j & 1)] = __uint_as_float(o[8 * w + j]) * inv;
+              if (direct) {
+                put(col8 + w, pack_bf162(e[0], e[1]), pack_bf162(e[2], e[3]), pack_bf162(e[4], e[5]), pack_bf162(e[6], e[7]));
+              } else {
+                const uint32_t piece = 2u * ((col8 + w) & 7u);
+                put(piece, __float_as_uint(e[0]), __float_as_uint(e[1]), __float_as_uint(e[2]), __float_as_uint(e[3]));
+                put(piece + 1, __float_as_uint(e[4]), __float_as_uint(e[5]), __float_as_uint(e[6]), __float_as_uint(e[7]));
+              }
+            }
           }
         }
-        if (!direct && (q & 1))
-          flush(16, reinterpret_cast<uint8_t*>(sp.part_o + static_cast<int64_t>(split) * D + 32 * (q - 1)), static_cast<int64_t>(sp.splits) * D * 4);
+        if (direct) flush(D / 8, reinterpret_cast<uint8_t*>(p.out), D * 2);
+        else flush(16, reinterpret_cast<uint8_t*>(sp.part_o + static_cast<int64_t>(split) * D + 64 * pp), static_cast<int64_t>(sp.splits) * D * 4);
       }
-      if (direct) flush(D / 8, reinterpret_cast<uint8_t*>(p.out), D * 2);
-      if (live) {
+      if (live && kh == 0) {
         if (used_splits > 1) sp.part_lse[orow * sp.splits + split] = lse2;
         else if (p.lse) p.lse[orow] = lse2 * 0.6931471805599453f;
       }
