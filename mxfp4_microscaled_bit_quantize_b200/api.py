@@ -4,6 +4,7 @@ library's kernels; there is no CPU path."""
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 
 import torch
@@ -294,19 +295,55 @@ def cache_alloc(n_pages: int, Hkv: int, d: int, page_size: int = 16, device="cud
     return torch.zeros((n_pages, Hkv, 2, page_size, 17 * d // 32), dtype=torch.uint8, device=device)
 
 
+# The calls on the cache are made once per layer and token, so their checks are kept cheap: one pass over
+# the attributes of each tensor, the raw stream, and a device switch only where one is needed.
 def _cache(cache):
-    """(n_pages, Hkv, page_size, d) of a cache tensor."""
+    """(n_pages, Hkv, page_size, d, device index) of a cache tensor."""
     _need(cache, "cache", torch.uint8)
-    if cache.dim() != 5 or cache.shape[2] != 2 or cache.shape[4] % 17 != 0:
+    shape = cache.shape
+    if len(shape) != 5 or shape[2] != 2 or shape[4] % 17 != 0:
         raise ValueError("cache must be [n_pages, Hkv, 2, page_size, 17 d / 32]")
-    n_pages, Hkv, _, P, row = cache.shape
-    return n_pages, Hkv, P, row // 17 * 32
+    return shape[0], shape[1], shape[3], shape[4] // 17 * 32, cache.get_device()
 
 
-def _on(dev, **tensors) -> None:
-    for name, t in tensors.items():
-        if t.device != dev:
-            raise ValueError(f"{name} must be on {dev}, got {t.device}")
+def _at(t, name: str, dtype, dev: int, shape) -> None:
+    """t must be a contiguous tensor of this type and shape on CUDA device `dev`."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev or not t.is_cuda:
+        raise ValueError(f"{name} must be a tensor on cuda:{dev}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _rows(t, name: str, heads, d: int, dev: int):
+    """(tokens, heads, strides) of bf16 rows [T, heads, d] on CUDA device `dev`; the rows themselves are contiguous."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev or not t.is_cuda:
+        raise ValueError(f"{name} must be a tensor on cuda:{dev}")
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    shape = t.shape
+    if len(shape) != 3 or (heads is not None and shape[1] != heads) or shape[2] != d:
+        raise ValueError(f"{name} must be [T, heads, {d}], got {tuple(shape)}")
+    stride = t.stride()
+    if stride[2] != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return shape[0], shape[1], stride
+
+
+def _call(name: str, dev: int, *args) -> None:
+    """The entry point `name` on CUDA device `dev` and its current stream (the last argument of every call)."""
+    fn = getattr(_lib.load(), name)
+    stream = torch._C._cuda_getCurrentRawStream(dev)
+    if torch.cuda.current_device() == dev:
+        st = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, stream)
+    if st != 0:
+        _lib.check(st, name)
 
 
 def mxattn_cache_plan(ctx_len, new_len, block_table, free_pages, page_size: int, max_tokens: int, out=None):
@@ -317,89 +354,62 @@ def mxattn_cache_plan(ctx_len, new_len, block_table, free_pages, page_size: int,
     info [4] int32: new tokens, free pages taken, requests refused, 0); `out` takes the same four to be written in
     place. A request that does not fit (rows past max_tokens, pages past the table or the free list) is refused:
     its slots are -1, as are those behind the last request."""
-    for t, n in ((ctx_len, "ctx_len"), (new_len, "new_len"), (block_table, "block_table"), (free_pages, "free_pages")):
-        _need(t, n, torch.int32)
-    dev = ctx_len.device
-    R = ctx_len.numel()
-    if ctx_len.dim() != 1 or new_len.shape != ctx_len.shape or block_table.dim() != 2 or block_table.shape[0] != R:
-        raise ValueError("ctx_len, new_len must be [R] and block_table [R, width]")
-    if free_pages.dim() != 1 or max_tokens < 0:
-        raise ValueError("free_pages must be [F] and max_tokens not negative")
-    _on(dev, new_len=new_len, block_table=block_table, free_pages=free_pages)
+    _need(block_table, "block_table", torch.int32)
+    dev = block_table.get_device()
+    if block_table.dim() != 2 or max_tokens < 0:
+        raise ValueError("block_table must be [R, width] and max_tokens not negative")
+    R, width = block_table.shape
+    _at(ctx_len, "ctx_len", torch.int32, dev, (R,))
+    _at(new_len, "new_len", torch.int32, dev, (R,))
+    n_free = free_pages.numel()
+    _at(free_pages, "free_pages", torch.int32, dev, (n_free,))
     if out is None:
-        ints = torch.empty(2 * R + 5, dtype=torch.int32, device=dev)
-        q_start, kv_len, info = ints[:R + 1], ints[R + 1:2 * R + 1], ints[2 * R + 1:]
-        slots = torch.empty(max_tokens, dtype=torch.int64, device=dev)
+        ints = torch.empty(2 * R + 5, dtype=torch.int32, device=block_table.device)
+        q_start, kv_len, info = torch.split_with_sizes(ints, (R + 1, R, 4))
+        slots = torch.empty(max_tokens, dtype=torch.int64, device=block_table.device)
     else:
         q_start, kv_len, slots, info = out
-        for t, shape, dt, n in ((q_start, (R + 1,), torch.int32, "q_start"), (kv_len, (R,), torch.int32, "kv_len"),
-                                (slots, (max_tokens,), torch.int64, "slots"), (info, (4,), torch.int32, "info")):
-            _need(t, n, dt)
-            if tuple(t.shape) != shape:
-                raise ValueError(f"{n} must have shape {shape}, got {tuple(t.shape)}")
-            _on(dev, **{n: t})
-    with torch.cuda.device(dev):
-        st = _lib.load().mxattn_cache_plan(ctx_len.data_ptr(), new_len.data_ptr(), R, block_table.data_ptr(),
-                                           block_table.shape[1], free_pages.data_ptr(), free_pages.numel(), page_size,
-                                           q_start.data_ptr(), kv_len.data_ptr(), slots.data_ptr(), max_tokens,
-                                           info.data_ptr(), _stream(dev))
-    _lib.check(st, "mxattn_cache_plan")
+        _at(q_start, "q_start", torch.int32, dev, (R + 1,))
+        _at(kv_len, "kv_len", torch.int32, dev, (R,))
+        _at(slots, "slots", torch.int64, dev, (max_tokens,))
+        _at(info, "info", torch.int32, dev, (4,))
+    _call("mxattn_cache_plan", dev, ctx_len.data_ptr(), new_len.data_ptr(), R, block_table.data_ptr(), width,
+          free_pages.data_ptr(), n_free, page_size, q_start.data_ptr(), kv_len.data_ptr(), slots.data_ptr(), max_tokens,
+          info.data_ptr())
     return q_start, kv_len, slots, info
-
-
-def _rows(t, name, H, d):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.bfloat16:
-        raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.dim() != 3 or (H is not None and t.shape[1] != H) or t.shape[2] != d or t.stride(2) != 1:
-        raise ValueError(f"{name} must be [T, heads, {d}] with contiguous rows, got {tuple(t.shape)}")
 
 
 def mxattn_cache_append(k, v, slots, cache, scale_mode: int = SCALE_UOS) -> None:
     """Quantize k, v [T, Hkv, d] (bf16, rows contiguous, any token and head strides) into the cache's slots
     (int64 [T]; a slot outside the cache skips its token; slots of one call must differ)."""
-    n_pages, Hkv, P, d = _cache(cache)
-    _need(slots, "slots", torch.int64)
-    _rows(k, "k", Hkv, d)
-    _rows(v, "v", Hkv, d)
-    T = k.shape[0]
-    if v.shape[0] != T or slots.dim() != 1 or slots.shape[0] != T:
-        raise ValueError("k, v and slots must have the same number of tokens")
-    dev = cache.device
-    _on(dev, k=k, v=v, slots=slots)
-    with torch.cuda.device(dev):
-        st = _lib.load().mxattn_cache_append(k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0),
-                                             v.stride(1), slots.data_ptr(), T, Hkv, d, P, n_pages, int(scale_mode),
-                                             cache.data_ptr(), _stream(dev))
-    _lib.check(st, "mxattn_cache_append")
+    n_pages, Hkv, P, d, dev = _cache(cache)
+    T, _, ks = _rows(k, "k", Hkv, d, dev)
+    Tv, _, vs = _rows(v, "v", Hkv, d, dev)
+    if Tv != T:
+        raise ValueError("k and v must have the same number of tokens")
+    _at(slots, "slots", torch.int64, dev, (T,))
+    _call("mxattn_cache_append", dev, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], slots.data_ptr(), T, Hkv, d,
+          P, n_pages, int(scale_mode), cache.data_ptr())
 
 
 def mxattn_cache_read(cache, slots, out=None):
     """(k, v) [T, Hkv, d] bf16: the values that the slots (int64 [T]) hold; zeros for slots outside the cache."""
-    n_pages, Hkv, P, d = _cache(cache)
-    _need(slots, "slots", torch.int64)
-    if slots.dim() != 1:
-        raise ValueError("slots must be [T]")
-    T, dev = slots.shape[0], cache.device
-    _on(dev, slots=slots)
+    n_pages, Hkv, P, d, dev = _cache(cache)
+    T = slots.numel()
+    _at(slots, "slots", torch.int64, dev, (T,))
     if out is None:
-        k, v = torch.empty((2, T, Hkv, d), dtype=torch.bfloat16, device=dev).unbind(0)
+        k, v = torch.empty((2, T, Hkv, d), dtype=torch.bfloat16, device=cache.device).unbind(0)
     else:
         k, v = out
-        for t, n in ((k, "k"), (v, "v")):
-            _need(t, n)
-            if tuple(t.shape) != (T, Hkv, d):
-                raise ValueError(f"{n} must have shape {(T, Hkv, d)}, got {tuple(t.shape)}")
-        _on(dev, k=k, v=v)
-    with torch.cuda.device(dev):
-        st = _lib.load().mxattn_cache_read(cache.data_ptr(), slots.data_ptr(), T, Hkv, d, P, n_pages, k.data_ptr(),
-                                           v.data_ptr(), _stream(dev))
-    _lib.check(st, "mxattn_cache_read")
+        _at(k, "k", torch.bfloat16, dev, (T, Hkv, d))
+        _at(v, "v", torch.bfloat16, dev, (T, Hkv, d))
+    _call("mxattn_cache_read", dev, cache.data_ptr(), slots.data_ptr(), T, Hkv, d, P, n_pages, k.data_ptr(), v.data_ptr())
     return k, v
 
 
+@functools.lru_cache(maxsize=256)
 def paged_workspace_size(T: int, R: int, Hq: int, Hkv: int, d: int, max_new: int, max_kv: int) -> int:
+    """Bytes of workspace that mxattn_paged_forward needs; 0 for unsupported shapes."""
     return int(_lib.load().mxattn_paged_workspace_size(T, R, Hq, Hkv, d, max_new, max_kv))
 
 
@@ -412,45 +422,32 @@ def mxattn_paged_forward(q, cache, block_table, q_start, kv_len, max_new: int, m
     upper bounds of a request's new tokens and of kv_len (default: what the table holds). causal: token i of n sees
     keys up to kv_len - n + i; otherwise all kv_len (cross attention). Returns out [T, Hq, d] bf16; rows of no
     request are left as they were (whatever they held, in a new `out`). lse: optional fp32 [T, Hq] to be written."""
-    n_pages, Hkv, P, d = _cache(cache)
-    _rows(q, "q", None, d)
-    for t, n in ((block_table, "block_table"), (q_start, "q_start"), (kv_len, "kv_len")):
-        _need(t, n, torch.int32)
-    T, Hq = q.shape[0], q.shape[1]
-    R, dev = kv_len.numel(), cache.device
-    if block_table.dim() != 2 or block_table.shape[0] != R or kv_len.dim() != 1 or tuple(q_start.shape) != (R + 1,):
-        raise ValueError("block_table must be [R, width], q_start [R + 1] and kv_len [R]")
-    _on(dev, q=q, block_table=block_table, q_start=q_start, kv_len=kv_len)
-    width = block_table.shape[1]
+    n_pages, Hkv, P, d, dev = _cache(cache)
+    T, Hq, qs = _rows(q, "q", None, d, dev)
+    _need(block_table, "block_table", torch.int32)
+    if block_table.dim() != 2 or block_table.get_device() != dev:
+        raise ValueError(f"block_table must be [R, width] on cuda:{dev}")
+    R, width = block_table.shape
+    _at(q_start, "q_start", torch.int32, dev, (R + 1,))
+    _at(kv_len, "kv_len", torch.int32, dev, (R,))
     if max_kv is None:
         max_kv = width * P
     if out is None:
-        out = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=dev)
+        out = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=cache.device)
     else:
-        _need(out, "out")
-        if tuple(out.shape) != (T, Hq, d):
-            raise ValueError(f"out must have shape {(T, Hq, d)}, got {tuple(out.shape)}")
-        _on(dev, out=out)
+        _at(out, "out", torch.bfloat16, dev, (T, Hq, d))
     if lse is not None:
-        _need(lse, "lse", torch.float32)
-        if tuple(lse.shape) != (T, Hq):
-            raise ValueError(f"lse must have shape {(T, Hq)}, got {tuple(lse.shape)}")
-        _on(dev, lse=lse)
-    lib = _lib.load()
+        _at(lse, "lse", torch.float32, dev, (T, Hq))
     if workspace is None:
-        n = int(lib.mxattn_paged_workspace_size(T, R, Hq, Hkv, d, max_new, max_kv))
+        n = paged_workspace_size(T, R, Hq, Hkv, d, max_new, max_kv)
         if n == 0:
             raise ValueError("unsupported attention shape")
-        workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+        workspace = torch.empty(n, dtype=torch.uint8, device=cache.device)
     else:
-        _need(workspace, "workspace", torch.uint8)
-        _on(dev, workspace=workspace)
-    with torch.cuda.device(dev):
-        st = lib.mxattn_paged_forward(q.data_ptr(), q.stride(0), q.stride(1), cache.data_ptr(), block_table.data_ptr(),
-                                      width, q_start.data_ptr(), kv_len.data_ptr(), out.data_ptr(),
-                                      None if lse is None else lse.data_ptr(), T, R, Hq, Hkv, d, P, n_pages, max_new,
-                                      max_kv, int(bool(causal)), workspace.data_ptr(), workspace.numel(), _stream(dev))
-    _lib.check(st, "mxattn_paged_forward")
+        _at(workspace, "workspace", torch.uint8, dev, (workspace.numel(),))
+    _call("mxattn_paged_forward", dev, q.data_ptr(), qs[0], qs[1], cache.data_ptr(), block_table.data_ptr(), width,
+          q_start.data_ptr(), kv_len.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(), T, R, Hq, Hkv, d,
+          P, n_pages, max_new, max_kv, 1 if causal else 0, workspace.data_ptr(), workspace.numel())
     return out
 
 

@@ -37,36 +37,44 @@ template <int NB> struct Frag;          // what a lane holds of 16 keys
 template <> struct Frag<4> { uint4 k0, k1; uint2 ks; uint2 v[4]; uint4 vs; };
 template <> struct Frag<2> { uint2 k0, k1; uint32_t ks; uint32_t v[4]; uint2 vs; };
 
+// Where a lane's pieces of 16 keys lie behind the first code byte of the first of them: the codes of the
+// group are `lane` pieces of its K rows, ks / vs its scale rows, all constants of the launch.
+template <int NB>
+struct LaneOffsets {
+  uint32_t k, ks, v, vs;
+  __device__ __forceinline__ LaneOffsets(uint32_t lane, int page_shift) {
+    const uint32_t g = lane >> 2, c = lane & 3u;
+    const uint32_t codes = (16u * NB) << page_shift, chunk = codes + (static_cast<uint32_t>(NB) << page_shift);
+    k = lane * (4u * NB);
+    ks = codes + g * (2u * NB);
+    v = chunk + 2u * c * (16u * NB) + g * (2u * NB);
+    vs = chunk + codes + c * (4u * NB);
+  }
+};
 // kc: the page's K chunk of this head; off: first of the 16 tokens in the page.
-__device__ __forceinline__ void load_frag(Frag<4>& f, const uint8_t* kc, uint32_t off, int page_shift, uint32_t lane) {
-  const uint32_t g = lane >> 2, c = lane & 3u;
-  const uint8_t* k = kc + off * 64u + lane * 16u;
-  f.k0 = ldg16(k);
-  f.k1 = ldg16(k + 512);
-  const uint32_t codes = 64u << page_shift;
-  f.ks = ldg8(kc + codes + off * 4u + g * 8u);
-  const uint8_t* vc = kc + codes + (4u << page_shift);
-  const uint8_t* v = vc + (off + 2u * c) * 64u + g * 8u;
+__device__ __forceinline__ void load_frag(Frag<4>& f, const uint8_t* kc, uint32_t off, const LaneOffsets<4>& at) {
+  const uint8_t *row = kc + off * 64u, *sc = kc + off * 4u;
+  f.k0 = ldg16(row + at.k);
+  f.k1 = ldg16(row + at.k + 512);
+  f.ks = ldg8(sc + at.ks);
+  f.vs = ldg16(sc + at.vs);
+  const uint8_t* v = row + at.v;
   f.v[0] = ldg8(v);
   f.v[1] = ldg8(v + 64);
   f.v[2] = ldg8(v + 512);
   f.v[3] = ldg8(v + 576);
-  f.vs = ldg16(vc + codes + off * 4u + c * 16u);
 }
-__device__ __forceinline__ void load_frag(Frag<2>& f, const uint8_t* kc, uint32_t off, int page_shift, uint32_t lane) {
-  const uint32_t g = lane >> 2, c = lane & 3u;
-  const uint8_t* k = kc + off * 32u + lane * 8u;
-  f.k0 = ldg8(k);
-  f.k1 = ldg8(k + 256);
-  const uint32_t codes = 32u << page_shift;
-  f.ks = ldg4(kc + codes + off * 2u + g * 4u);
-  const uint8_t* vc = kc + codes + (2u << page_shift);
-  const uint8_t* v = vc + (off + 2u * c) * 32u + g * 4u;
+__device__ __forceinline__ void load_frag(Frag<2>& f, const uint8_t* kc, uint32_t off, const LaneOffsets<2>& at) {
+  const uint8_t *row = kc + off * 32u, *sc = kc + off * 2u;
+  f.k0 = ldg8(row + at.k);
+  f.k1 = ldg8(row + at.k + 256);
+  f.ks = ldg4(sc + at.ks);
+  f.vs = ldg8(sc + at.vs);
+  const uint8_t* v = row + at.v;
   f.v[0] = ldg4(v);
   f.v[1] = ldg4(v + 32);
   f.v[2] = ldg4(v + 256);
   f.v[3] = ldg4(v + 288);
-  f.vs = ldg8(vc + codes + off * 2u + c * 8u);
 }
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -125,6 +133,16 @@ __device__ __forceinline__ void v_scale_pairs(const Frag<2>& f, uint32_t (&s)[2]
     s[0][h] = a & 0x00FF00FFu;
     s[1][h] = (a >> 8) & 0x00FF00FFu;
   }
+}
+
+// Nonzero where a scale byte of the lane's four keys is not within [r - 14, r + 1], r the reference byte of
+// its block (packed in `top` as r + 1). The subtraction borrows only above the first byte that is out of
+// range, which itself shows (for bytes up to r + 240; larger ones are V values past 2^112).
+__device__ __forceinline__ uint32_t v_out_of_range(const Frag<4>& f, uint32_t top) {
+  return ((top - f.vs.x) | (top - f.vs.y) | (top - f.vs.z) | (top - f.vs.w)) & 0xF0F0F0F0u;
+}
+__device__ __forceinline__ uint32_t v_out_of_range(const Frag<2>& f, uint32_t top) {
+  return ((top - f.vs.x) | (top - f.vs.y)) & 0xF0F0F0F0u;      // two keys a word: `top` holds the two blocks twice
 }
 
 template <int D, int NT>
@@ -200,11 +218,16 @@ __global__ void __launch_bounds__(kSmallWarps * 32, NT == 1 ? 4 : 2) paged_small
   const int first = static_cast<int>(split * sp.chunk) >> 4;
   const int stop = (min(lim_max, static_cast<int>(min((split + 1) * sp.chunk, static_cast<int64_t>(0x7FFFFFFF)))) + 15) >> 4;
   const int32_t* table = p.block_table + static_cast<int64_t>(r) * p.table_width;
-  const int64_t head_bytes = 2ll * cache_chunk_bytes(D, 1u << p.page_shift);
-  const uint32_t page_mask = (1u << p.page_shift) - 1u;
+  const uint32_t n_pages = static_cast<uint32_t>(p.n_pages), page_mask = (1u << p.page_shift) - 1u;
+  const uint32_t head_bytes = 2u * cache_chunk_bytes(D, 1u << p.page_shift);
+  const uint64_t page_bytes = static_cast<uint64_t>(p.Hkv) * head_bytes;
+  const uint8_t* base = p.cache + static_cast<uint64_t>(head) * head_bytes;
+  const LaneOffsets<NB> at(lane, p.page_shift);
 
+  // Scores stay in units of the columns' qscale: thr is the raw score that moves a reference, mu7 = m - 7
+  // (0 while the column has seen no key, so that 2^(-inf - mu7) is 0 and not NaN).
   float o[NT][2 * NB][4];
-  float l[NT][2], m[NT][2], mu[NT][2];       // mu: m, or 0 while the column has seen no key
+  float l[NT][2], m[NT][2], mu7[NT][2], thr[NT][2];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -212,215 +235,198 @@ __global__ void __launch_bounds__(kSmallWarps * 32, NT == 1 ? 4 : 2) paged_small
 #pragma unroll
       for (int x = 0; x < 4; ++x) o[nt][t][x] = 0.f;
 #pragma unroll
-    for (int x = 0; x < 2; ++x) { l[nt][x] = 0.f; m[nt][x] = -INFINITY; mu[nt][x] = 0.f; }
+    for (int x = 0; x < 2; ++x) { l[nt][x] = 0.f; m[nt][x] = -INFINITY; mu7[nt][x] = 0.f; thr[nt][x] = -INFINITY; }
   }
   int rb[NB];                                 // reference exponent byte of V's channel blocks
+  uint32_t rb_top = 0u, sc_add[NB];           // the blocks' r + 1 packed; 2^(s - r) as fp16 bits is s 1024 + sc_add
 #pragma unroll
-  for (int b = 0; b < NB; ++b) rb[b] = -1;
+  for (int b = 0; b < NB; ++b) { rb[b] = -1; sc_add[b] = 0x04000400u * 16u; }
 
-  // one group ahead in registers, its page looked up one group earlier still
   auto page_of = [&](int grp) -> int {
     return grp < stop ? __ldg(table + ((grp << 4) >> p.page_shift)) : -1;     // looked at when it is used: a comparison would wait
   };
-  const uint32_t n_pages = static_cast<uint32_t>(p.n_pages);
   auto fetch = [&](Frag<NB>& f, int grp, int page) {
     if (static_cast<uint32_t>(page) < n_pages)
-      load_frag(f, p.cache + (static_cast<int64_t>(page) * p.Hkv + head) * head_bytes, (static_cast<uint32_t>(grp) << 4) & page_mask, p.page_shift, lane);
+      load_frag(f, base + static_cast<uint32_t>(page) * page_bytes, (static_cast<uint32_t>(grp) << 4) & page_mask, at);
   };
-  int grp = first + static_cast<int>(warp);
-  int page = page_of(grp), page_next = page_of(grp + kSmallWarps);
-  Frag<NB> f, fn;
-  fetch(f, grp, page);
-  for (; grp < stop; grp += kSmallWarps) {
-    fetch(fn, grp + kSmallWarps, page_next);
-    const int page_after = page_of(grp + 2 * kSmallWarps);
-    if (static_cast<uint32_t>(page) < n_pages) {
-      const int key0 = grp << 4;
-      // ---- S^T: partial scores of each 32-channel block, times the block's scale
-      float s[NT][4];
+  auto step = [&](Frag<NB>& f, int grp) {
+    const int key0 = grp << 4;
+    // ---- S^T: partial scores of each 32-channel block, times the block's scale
+    float s[NT][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) s[nt][x] = 0.f;
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        uint32_t a[4], a8[4];
-        e2m1x8_to_half2(word_of(f.k0, b), a);
-        e2m1x8_to_half2(word_of(f.k1, b), a8);
-        float s0, s1;
-        k_scales(f, b, s0, s1);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float acc[4];
-          mma_f16_zero(acc, a[0], a8[0], a[1], a8[1], qf[nt][b][0], qf[nt][b][1]);
-          mma_f16(acc, a[2], a8[2], a[3], a8[3], qf[nt][b][2], qf[nt][b][3]);
-          s[nt][0] = fmaf(acc[0], s0, s[nt][0]);
-          s[nt][1] = fmaf(acc[1], s0, s[nt][1]);
-          s[nt][2] = fmaf(acc[2], s1, s[nt][2]);
-          s[nt][3] = fmaf(acc[3], s1, s[nt][3]);
-        }
-      }
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) s[nt][x] *= qscale[nt][x & 1];
-      if (key0 + 16 > lim_min) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-            if (key0 + static_cast<int>(g) + (x >> 1) * 8 >= lim[nt][x & 1]) s[nt][x] = -INFINITY;
-      }
-      // ---- the columns' references: moved only when a score passes one by 7
-      bool up = false;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int x = 0; x < 2; ++x) up |= fmaxf(s[nt][x], s[nt][x + 2]) > m[nt][x] + 7.f;
-      if (__any_sync(0xffffffffu, up)) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            float t = fmaxf(s[nt][x], s[nt][x + 2]);
-            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
-            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
-            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
-            const float mn = fmaxf(m[nt][x], t);
-            const float mun = mn == -INFINITY ? 0.f : mn;
-            const float alpha = m[nt][x] == -INFINITY ? 0.f : ex2(m[nt][x] - mun);
-            m[nt][x] = mn;
-            mu[nt][x] = mun;
-            l[nt][x] *= alpha;
-#pragma unroll
-            for (int tt = 0; tt < 2 * NB; ++tt) { o[nt][tt][x] *= alpha; o[nt][tt][x + 2] *= alpha; }
-          }
-      }
-      // ---- p = 2^(x - m + 7), summed in fp32; as fp16 the other way round (key pairs of column g)
-      float pv[NT][4];
+    for (int b = 0; b < NB; ++b) {
+      uint32_t a[4], a8[4];
+      e2m1x8_to_half2(word_of(f.k0, b), a);
+      e2m1x8_to_half2(word_of(f.k1, b), a8);
+      float s0, s1;
+      k_scales(f, b, s0, s1);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
+        float acc[4];
+        mma_f16_zero(acc, a[0], a8[0], a[1], a8[1], qf[nt][b][0], qf[nt][b][1]);
+        mma_f16(acc, a[2], a8[2], a[3], a8[3], qf[nt][b][2], qf[nt][b][3]);
 #pragma unroll
-        for (int x = 0; x < 4; ++x) pv[nt][x] = ex2(s[nt][x] - mu[nt][x & 1] + 7.f);
-        l[nt][0] += pv[nt][0] + pv[nt][2];
-        l[nt][1] += pv[nt][1] + pv[nt][3];
+        for (int x = 0; x < 4; ++x) s[nt][x] = b == 0 ? acc[x] * (x < 2 ? s0 : s1) : fmaf(acc[x], x < 2 ? s0 : s1, s[nt][x]);
       }
-      // ---- V's scales relative to the reference exponents
-      uint32_t vs[NB][2];
-      v_scale_pairs(f, vs);
-      if (key0 + 16 > lim_max) {              // tokens behind the end: whatever their bytes say
+    }
+    if (key0 + 16 > lim_min) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t keep = (key0 + 8 * h + 2 * static_cast<int>(c) < lim_max ? 0xFFFFu : 0u) |
-                                (key0 + 8 * h + 2 * static_cast<int>(c) + 1 < lim_max ? 0xFFFF0000u : 0u);
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int b = 0; b < NB; ++b) vs[b][h] &= keep;
+        for (int x = 0; x < 4; ++x)
+          if (key0 + static_cast<int>(g) + (x >> 1) * 8 >= lim[nt][x & 1]) s[nt][x] = -INFINITY;
+    }
+    // ---- the columns' references: moved only when a score passes one by 7
+    bool up = false;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) up |= fmaxf(s[nt][x], s[nt][x + 2]) > thr[nt][x];
+    if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          float t = fmaxf(s[nt][x], s[nt][x + 2]);
+          t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
+          t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
+          t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16)) * qscale[nt][x];
+          const float mn = fmaxf(m[nt][x], t);
+          const float alpha = m[nt][x] == -INFINITY ? 0.f : ex2(m[nt][x] - mn);
+          m[nt][x] = mn;
+          mu7[nt][x] = mn == -INFINITY ? 0.f : mn - 7.f;
+          thr[nt][x] = (mn + 7.f) / qscale[nt][x];
+          l[nt][x] *= alpha;
+#pragma unroll
+          for (int tt = 0; tt < 2 * NB; ++tt) { o[nt][tt][x] *= alpha; o[nt][tt][x + 2] *= alpha; }
         }
+    }
+    // ---- p = 2^(x - m + 7), summed in fp32
+    float pv[NT][4];
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {        // ... they take the largest exponent there is
-          uint32_t t = max(max(vs[b][0] & 0xFFFFu, vs[b][0] >> 16), max(vs[b][1] & 0xFFFFu, vs[b][1] >> 16));
-          t = max(__reduce_max_sync(0xffffffffu, t), static_cast<uint32_t>(max(rb[b], 0)));
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int x = 0; x < 4; ++x) pv[nt][x] = ex2(fmaf(s[nt][x], qscale[nt][x & 1], -mu7[nt][x & 1]));
+      l[nt][0] += pv[nt][0] + pv[nt][2];
+      l[nt][1] += pv[nt][1] + pv[nt][3];
+    }
+    // ---- V's scales relative to the reference exponents
+    uint32_t vs[NB][2];
+    v_scale_pairs(f, vs);
+    bool wide = false;
+    const bool tail = key0 + 16 > lim_max;
+    if (__any_sync(0xffffffffu, v_out_of_range(f, rb_top) != 0u) || tail) {
+      // a scale above the reference moves it (O is scaled down); one far below takes the wide path
+      rb_top = 0u;
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        if (tail) {                           // tokens behind the end, whatever their bytes say: no scale at all
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            vs[b][h] &= (key0 + 8 * h + 2 * static_cast<int>(c) < lim_max ? 0xFFFFu : 0u) |
+                        (key0 + 8 * h + 2 * static_cast<int>(c) + 1 < lim_max ? 0xFFFF0000u : 0u);
+        }
+        const int t = static_cast<int>(__reduce_max_sync(0xffffffffu, max(max(vs[b][0] & 0xFFFFu, vs[b][0] >> 16), max(vs[b][1] & 0xFFFFu, vs[b][1] >> 16))));
+        const int r_new = max(rb[b], t);
+        if (tail) {                           // ... and then the reference's, under p = 0
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            if (key0 + 8 * h + 2 * static_cast<int>(c) >= lim_max) vs[b][h] |= t;
-            if (key0 + 8 * h + 2 * static_cast<int>(c) + 1 >= lim_max) vs[b][h] |= t << 16;
+            if (key0 + 8 * h + 2 * static_cast<int>(c) >= lim_max) vs[b][h] |= static_cast<uint32_t>(r_new);
+            if (key0 + 8 * h + 2 * static_cast<int>(c) + 1 >= lim_max) vs[b][h] |= static_cast<uint32_t>(r_new) << 16;
           }
         }
-      }
-      // d = s - rb + 14 lies in [0, 15] for scales from 2^-14 to 2 of the reference
-      uint32_t rel[NB][2], out_of_range = 0;
+        const int lo = static_cast<int>(__reduce_min_sync(0xffffffffu, min(min(vs[b][0] & 0xFFFFu, vs[b][0] >> 16), min(vs[b][1] & 0xFFFFu, vs[b][1] >> 16))));
+        if (r_new > rb[b]) {
+          const float down = rb[b] < 0 ? 0.f : exp2f(static_cast<float>(rb[b] - r_new));
 #pragma unroll
-      for (int b = 0; b < NB; ++b)
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          rel[b][h] = vs[b][h] - static_cast<uint32_t>(rb[b] - 14) * 0x00010001u;
-          out_of_range |= rel[b][h];
+            for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+              for (int x = 0; x < 4; ++x) o[nt][2 * b + tt][x] *= down;
+          rb[b] = r_new;
         }
-      bool wide = false;
-      if (__any_sync(0xffffffffu, (out_of_range & 0xFFF0FFF0u) != 0u)) {
-        // a scale above the reference moves it (O is scaled down); one far below takes the wide path
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          const int t = static_cast<int>(__reduce_max_sync(0xffffffffu, max(max(vs[b][0] & 0xFFFFu, vs[b][0] >> 16), max(vs[b][1] & 0xFFFFu, vs[b][1] >> 16))));
-          const int lo = static_cast<int>(__reduce_min_sync(0xffffffffu, min(min(vs[b][0] & 0xFFFFu, vs[b][0] >> 16), min(vs[b][1] & 0xFFFFu, vs[b][1] >> 16))));
-          if (t > rb[b]) {
-            const float down = rb[b] < 0 ? 0.f : exp2f(static_cast<float>(rb[b] - t));
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int tt = 0; tt < 2; ++tt)
-#pragma unroll
-                for (int x = 0; x < 4; ++x) o[nt][2 * b + tt][x] *= down;
-            rb[b] = t;
-          }
-          wide |= lo < rb[b] - 14;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) rel[b][h] = vs[b][h] - static_cast<uint32_t>(rb[b] - 14) * 0x00010001u;
-        }
+        wide |= lo < rb[b] - 14;
+        rb_top |= static_cast<uint32_t>(min(rb[b] + 1, 255)) << (8 * b);
+        sc_add[b] = static_cast<uint32_t>(15 - rb[b]) * 0x04000400u;
       }
-      uint32_t pt[NT][2];
+      if (NB == 2) rb_top |= rb_top << 16;
+    }
+    // ---- P^T (key pairs of column g): fp16 in general, bf16 on the wide path
+    uint32_t pt[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
       if (!wide) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          pt[nt][0] = transpose8x8(pack_half2(pv[nt][0], pv[nt][1]));
-          pt[nt][1] = transpose8x8(pack_half2(pv[nt][2], pv[nt][3]));
-        }
+        pt[nt][0] = transpose8x8(pack_half2(pv[nt][0], pv[nt][1]));
+        pt[nt][1] = transpose8x8(pack_half2(pv[nt][2], pv[nt][3]));
       } else {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          pt[nt][0] = transpose8x8(pack_bf162(pv[nt][0], pv[nt][1]));
-          pt[nt][1] = transpose8x8(pack_bf162(pv[nt][2], pv[nt][3]));
-        }
+        pt[nt][0] = transpose8x8(pack_bf162(pv[nt][0], pv[nt][1]));
+        pt[nt][1] = transpose8x8(pack_bf162(pv[nt][2], pv[nt][3]));
       }
-      // ---- O^T += V^T P^T. Words w of a key pair hold blocks 2w, 2w + 1; nibbles of the two keys are
-      //      brought together so that one cvt gives the pair of one channel.
+    }
+    // ---- O^T += V^T P^T. Words w of a key pair hold blocks 2w, 2w + 1; nibbles of the two keys are
+    //      brought together so that one cvt gives the pair of one channel.
 #pragma unroll
-      for (int w = 0; w < NB / 2; ++w) {
-        uint32_t ev[2][4], od[2][4];          // [key pair][2 (block & 1) + tile]: rows g and g + 8
+    for (int w = 0; w < NB / 2; ++w) {
+      uint32_t ev[2][4], od[2][4];            // [key pair][2 (block & 1) + tile]: rows g and g + 8
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t x = word_of(f.v[2 * h], w), y = word_of(f.v[2 * h + 1], w);
-          e2m1x8_to_half2((x & 0x0F0F0F0Fu) | ((y << 4) & 0xF0F0F0F0u), ev[h]);
-          e2m1x8_to_half2(((x >> 4) & 0x0F0F0F0Fu) | (y & 0xF0F0F0F0u), od[h]);
-        }
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t x = word_of(f.v[2 * h], w), y = word_of(f.v[2 * h + 1], w);
+        e2m1x8_to_half2((x & 0x0F0F0F0Fu) | ((y << 4) & 0xF0F0F0F0u), ev[h]);
+        e2m1x8_to_half2(((x >> 4) & 0x0F0F0F0Fu) | (y & 0xF0F0F0F0u), od[h]);
+      }
 #pragma unroll
-        for (int bb = 0; bb < 2; ++bb) {
-          const int b = 2 * w + bb;
-          if (!wide) {
-            const uint32_t sc0 = rel[b][0] * 1024u + 0x04000400u, sc1 = rel[b][1] * 1024u + 0x04000400u;   // 2^(s - rb)
+      for (int bb = 0; bb < 2; ++bb) {
+        const int b = 2 * w + bb;
+        if (!wide) {
+          const uint32_t sc0 = vs[b][0] * 1024u + sc_add[b], sc1 = vs[b][1] * 1024u + sc_add[b];   // 2^(s - r)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              const uint32_t b0 = hmul2(pt[nt][0], sc0), b1 = hmul2(pt[nt][1], sc1);
+          for (int nt = 0; nt < NT; ++nt) {
+            const uint32_t b0 = hmul2(pt[nt][0], sc0), b1 = hmul2(pt[nt][1], sc1);
 #pragma unroll
-              for (int t = 0; t < 2; ++t)
-                mma_f16(o[nt][2 * b + t], ev[0][2 * bb + t], od[0][2 * bb + t], ev[1][2 * bb + t], od[1][2 * bb + t], b0, b1);
-            }
-          } else {
-            // bf16 V relative to the reference: code 2^(s - rb), exact; P in bf16
-            uint32_t e2[2][2], o2[2][2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const float f0 = exp2f(static_cast<float>(static_cast<int>(vs[b][h] & 0xFFFFu) - rb[b]));
-              const float f1 = exp2f(static_cast<float>(static_cast<int>(vs[b][h] >> 16) - rb[b]));
-#pragma unroll
-              for (int t = 0; t < 2; ++t) {
-                const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&ev[h][2 * bb + t]));
-                const float2 z = __half22float2(*reinterpret_cast<const __half2*>(&od[h][2 * bb + t]));
-                e2[h][t] = pack_bf162(a.x * f0, a.y * f1);
-                o2[h][t] = pack_bf162(z.x * f0, z.y * f1);
-              }
-            }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int t = 0; t < 2; ++t) mma_bf16(o[nt][2 * b + t], e2[0][t], o2[0][t], e2[1][t], o2[1][t], pt[nt][0], pt[nt][1]);
+            for (int t = 0; t < 2; ++t)
+              mma_f16(o[nt][2 * b + t], ev[0][2 * bb + t], od[0][2 * bb + t], ev[1][2 * bb + t], od[1][2 * bb + t], b0, b1);
           }
+        } else {
+          // bf16 V relative to the reference: code 2^(s - r), exact; P in bf16
+          uint32_t e2[2][2], o2[2][2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float f0 = exp2f(static_cast<float>(static_cast<int>(vs[b][h] & 0xFFFFu) - rb[b]));
+            const float f1 = exp2f(static_cast<float>(static_cast<int>(vs[b][h] >> 16) - rb[b]));
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              const float2 aa = __half22float2(*reinterpret_cast<const __half2*>(&ev[h][2 * bb + t]));
+              const float2 zz = __half22float2(*reinterpret_cast<const __half2*>(&od[h][2 * bb + t]));
+              e2[h][t] = pack_bf162(aa.x * f0, aa.y * f1);
+              o2[h][t] = pack_bf162(zz.x * f0, zz.y * f1);
+            }
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int t = 0; t < 2; ++t) mma_bf16(o[nt][2 * b + t], e2[0][t], o2[0][t], e2[1][t], o2[1][t], pt[nt][0], pt[nt][1]);
         }
       }
     }
-    f = fn;
-    page = page_next;
+  };
+  // one group ahead in registers (two sets that change roles), its page looked up one group earlier still
+  int grp = first + static_cast<int>(warp);
+  int page = page_of(grp), page_next = page_of(grp + kSmallWarps);
+  Frag<NB> fa, fb;
+  fetch(fa, grp, page);
+  while (grp < stop) {
+    fetch(fb, grp + kSmallWarps, page_next);
+    int page_after = page_of(grp + 2 * kSmallWarps);
+    if (static_cast<uint32_t>(page) < n_pages) step(fa, grp);
+    grp += kSmallWarps;
+    if (grp >= stop) break;
+    page = page_after;
+    fetch(fa, grp + kSmallWarps, page);
+    page_after = page_of(grp + 2 * kSmallWarps);
+    if (static_cast<uint32_t>(page_next) < n_pages) step(fb, grp);
     page_next = page_after;
+    grp += kSmallWarps;
   }
 
   // ---- the warps' results meet in shared memory

@@ -426,9 +426,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const PagedPara
       const uint32_t gone = __ballot_sync(0xffffffffu, static_cast<uint32_t>(entry) >= n_pages && lane < 8 && key_begin + t * 128ll + lane * 16 < lim_all);
       entry = entry_of(t + 1);
       ok = warp_wait_tc(&s.bar_s_full[x], t & 1, abort_flag, p.status, kStatusTimeoutS | x);
-      // the tiles' exponentials take turns, so that one tile's products run under the other's softmax
-      const int before = x == 0 ? t - 1 : t;
-      if (ok && before >= 0 && before < n_other) ok = warp_wait_tc(&s.bar_turn[x], before & 1, abort_flag, p.status, kStatusTimeoutS | 4 | x);
       if (!ok) break;
       tc_fence_after();
       float v[64];                         // keys 64 kh .. of the tile
@@ -480,6 +477,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const PagedPara
         m = mn;
         mu = mun;
       }
+      // the tiles' exponentials take turns, so that one tile's products run under the other's softmax
+      const int before = x == 0 ? t - 1 : t;
+      if (before >= 0 && before < n_other) ok = warp_wait_tc(&s.bar_turn[x], before & 1, abort_flag, p.status, kStatusTimeoutS | 4 | x);
+      if (!ok) break;
 #pragma unroll
       for (int q = 0; q < 2; ++q) {        // 32 scores of each half become 16 columns of P, over S columns that are in registers
         uint32_t pk[16];
