@@ -36,6 +36,9 @@ constexpr int kConvWarp0 = 4, kRowWarp0 = 12;    // warps 0-3 issue, 4-11 conver
 constexpr uint32_t kTcCols = 512, kColSx = 0, kColOx = 256;   // S / P of tile X at 128 X, O at 256 + 128 X
 constexpr uint32_t kSw128 = 2;                                // descriptor code of the 128-byte swizzle
 constexpr int kTcStages = 2;
+// A row's reference moves when a score passes it by this much (in powers of two). bf16 has fp32's range, so
+// P = 2^32 costs no accuracy; O and l stay finite for V below 2^80.
+constexpr float kMoveBy = 32.f;
 
 template <int D>
 struct __align__(1024) TcSmem {
@@ -82,6 +85,24 @@ __device__ __forceinline__ bool mbar_poll(uint64_t* bar, uint32_t parity, volati
 }
 __device__ __forceinline__ bool warp_wait_tc(uint64_t* bar, uint32_t parity, volatile int* abort_flag, unsigned int* status, unsigned int code) {
   return __all_sync(0xffffffffu, mbar_poll(bar, parity, abort_flag, status, code));
+}
+// The same for the issuing warps, whose waits lie on the critical path: test_wait returns at once, where
+// try_wait sleeps and wakes late.
+__device__ __forceinline__ bool warp_spin_tc(uint64_t* bar, uint32_t parity, volatile int* abort_flag, unsigned int* status, unsigned int code) {
+  bool ok = mbar_test_wait(bar, parity);
+  if (!ok) {
+    const uint64_t t0 = global_timer_ns();
+    for (;;) {
+      for (int i = 0; i < 64 && !ok; ++i) ok = mbar_test_wait(bar, parity);
+      if (ok || *abort_flag) break;
+      if (global_timer_ns() - t0 > kWaitTimeoutNs) {
+        *abort_flag = 1;
+        atomicCAS(status, 0u, code);
+        break;
+      }
+    }
+  }
+  return __all_sync(0xffffffffu, ok);
 }
 __device__ __forceinline__ void drain_wait_tc(uint64_t* bar, uint32_t parity) {
   const uint64_t t0 = global_timer_ns();
@@ -264,9 +285,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const PagedPara
       const uint64_t d_v = smem_desc(0, 128 * 128, 1024, kSw128);         // MN-major: slabs 16 KB apart, 8 keys 1 KB
       const uint32_t a_q = smem_u32(s.q[x]) >> 4, a_k = smem_u32(s.k[0]) >> 4, a_v = smem_u32(s.v[0]) >> 4;
       const uint32_t t_s = tmem + kColSx + 128 * x, t_o = tmem + kColOx + 128 * x;
-      bool ok = n_own == 0 || warp_wait_tc(&s.bar_q, 0, abort_flag, p.status, kStatusTimeoutQ);
+      bool ok = n_own == 0 || warp_spin_tc(&s.bar_q, 0, abort_flag, p.status, kStatusTimeoutQ);
       auto wait_k = [&](int t) -> bool {
-        return warp_wait_tc(&s.bar_k_full[t % kTcStages], (t / kTcStages) & 1, abort_flag, p.status, kStatusTimeoutKV | (t % kTcStages));
+        return warp_spin_tc(&s.bar_k_full[t % kTcStages], (t / kTcStages) & 1, abort_flag, p.status, kStatusTimeoutKV | (t % kTcStages));
       };
       auto issue_s = [&](int t) {
         const int st = t % kTcStages;
@@ -289,8 +310,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const PagedPara
       }
       for (int t = 0; ok && t < n_own; ++t) {
         const int st = t % kTcStages;
-        ok = warp_wait_tc(&s.bar_v_full[st], (t / kTcStages) & 1, abort_flag, p.status, kStatusTimeoutKV | 8 | st) &&
-             warp_wait_tc(&s.bar_p_full[x], t & 1, abort_flag, p.status, kStatusTimeoutP | x);
+        ok = warp_spin_tc(&s.bar_v_full[st], (t / kTcStages) & 1, abort_flag, p.status, kStatusTimeoutKV | 8 | st) &&
+             warp_spin_tc(&s.bar_p_full[x], t & 1, abort_flag, p.status, kStatusTimeoutP | x);
         if (!ok) break;
         tc_fence_after();
         if (leader) {
@@ -304,7 +325,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const PagedPara
         __syncwarp();
         if (t + 1 < n_own) {
           // S(t + 1) overwrites the columns that hold P(t)
-          ok = wait_k(t + 1) && warp_wait_tc(&s.bar_pv[x], t & 1, abort_flag, p.status, kStatusTimeoutPV | x);
+          ok = wait_k(t + 1) && warp_spin_tc(&s.bar_pv[x], t & 1, abort_flag, p.status, kStatusTimeoutPV | x);
           if (ok) issue_s(t + 1);
         }
       }
@@ -456,7 +477,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const PagedPara
       a2 = fmax3(a2, v[62], v[63]);
       float top = fmaxf(fmax3(a0, a1, a2), a3);
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16)) * c;
-      const bool up = top > m + 8.f;
+      const bool up = top > m + kMoveBy;
       if (__any_sync(0xffffffffu, up)) {
         const float mn = up ? top : m;
         const float mun = mn == -INFINITY ? 0.f : mn;
