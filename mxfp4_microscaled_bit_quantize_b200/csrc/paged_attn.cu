@@ -32,49 +32,97 @@
 namespace mxattn {
 
 constexpr int kSmallWarps = 4;
+constexpr int kMaxSplits = 128;
+constexpr int kRingGroups = 4;          // groups of 16 keys in a warp's ring
 
 template <int NB> struct Frag;          // what a lane holds of 16 keys
-template <> struct Frag<4> { uint4 k0, k1; uint2 ks; uint2 v[4]; uint4 vs; };
-template <> struct Frag<2> { uint2 k0, k1; uint32_t ks; uint32_t v[4]; uint2 vs; };
+template <> struct Frag<4> { uint4 k0, k1; uint2 ks; };
+template <> struct Frag<2> { uint2 k0, k1; uint32_t ks; };
+template <int NB> struct VFrag;
+template <> struct VFrag<4> { uint2 v[4]; uint4 vs; };
+template <> struct VFrag<2> { uint32_t v[4]; uint2 vs; };
 
-// Where a lane's pieces of 16 keys lie behind the first code byte of the first of them: the codes of the
-// group are `lane` pieces of its K rows, ks / vs its scale rows, all constants of the launch.
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ uint2 ld_shared_v2(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_shared_u32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+
+// 16 keys in a warp's ring: K codes, V codes, K scales, V scales as they lie in the page (17 d bytes), but
+// for d = 128 the 16-byte pieces of V row t are at piece ^ (t / 2 % 4): a lane reads 8 bytes of rows 2c and
+// their neighbours, whose 64-byte rows would otherwise share banks four ways.
+template <int NB> constexpr uint32_t kGroupBytes = 16u * 17u * 2u * NB;
+
+// A lane's constants for copying groups into the ring and reading them back (byte offsets in the page's two
+// chunks of this head, and in a slot).
 template <int NB>
-struct LaneOffsets {
-  uint32_t k, ks, v, vs;
-  __device__ __forceinline__ LaneOffsets(uint32_t lane, int page_shift) {
+struct GroupLane {
+  uint32_t from_row, from_v, from_sc;         // K codes; V codes behind them; scales
+  uint32_t to_v, to_sc, k, v, ks, vs;
+  bool has_sc;                                // NB lanes copy K's scales, the next NB lanes V's
+  __device__ __forceinline__ GroupLane(uint32_t lane, int page_shift) {
+    constexpr uint32_t kRow = 16u * NB, kCodes = 16u * kRow;
     const uint32_t g = lane >> 2, c = lane & 3u;
-    const uint32_t codes = (16u * NB) << page_shift, chunk = codes + (static_cast<uint32_t>(NB) << page_shift);
+    const uint32_t codes = kRow << page_shift, chunk = codes + (static_cast<uint32_t>(NB) << page_shift);
+    from_row = lane * 16u;
+    from_v = chunk;
+    has_sc = lane < 2u * NB;
+    from_sc = lane < NB ? codes + lane * 16u : chunk + codes + (lane - NB) * 16u;
+    to_v = kCodes + (NB == 4 ? (lane ^ ((lane >> 3) & 3u)) << 4 : lane << 4);   // row lane / 4, piece (lane & 3) ^ (row / 2 % 4)
+    to_sc = 2u * kCodes + lane * 16u;
     k = lane * (4u * NB);
-    ks = codes + g * (2u * NB);
-    v = chunk + 2u * c * (16u * NB) + g * (2u * NB);
-    vs = chunk + codes + c * (4u * NB);
+    v = kCodes + (NB == 4 ? c * 128u + (((g >> 1) ^ c) << 4) + (g & 1u) * 8u : c * 64u + g * 4u);   // rows 2c, 2c + 1, 2c + 8, 2c + 9
+    ks = 2u * kCodes + g * (2u * NB);
+    vs = 2u * kCodes + 16u * NB + c * (4u * NB);
   }
 };
-// kc: the page's K chunk of this head; off: first of the 16 tokens in the page.
-__device__ __forceinline__ void load_frag(Frag<4>& f, const uint8_t* kc, uint32_t off, const LaneOffsets<4>& at) {
-  const uint8_t *row = kc + off * 64u, *sc = kc + off * 4u;
-  f.k0 = ldg16(row + at.k);
-  f.k1 = ldg16(row + at.k + 512);
-  f.ks = ldg8(sc + at.ks);
-  f.vs = ldg16(sc + at.vs);
-  const uint8_t* v = row + at.v;
-  f.v[0] = ldg8(v);
-  f.v[1] = ldg8(v + 64);
-  f.v[2] = ldg8(v + 512);
-  f.v[3] = ldg8(v + 576);
+// Copies 16 tokens into ring slot `dst`; kc: the page's K chunk of this head, off: the first token in the page.
+template <int NB>
+__device__ __forceinline__ void fetch_group(uint32_t dst, uint32_t lane, const GroupLane<NB>& at, const uint8_t* kc, uint32_t off) {
+  const uint8_t* row = kc + (off * (16u * NB) + at.from_row);
+  const uint8_t* vrow = row + at.from_v;
+  copy16(dst + lane * 16u, row);
+  copy16(dst + at.to_v, vrow);
+  if (NB == 4) {
+    copy16(dst + 512u + lane * 16u, row + 512);
+    copy16(dst + at.to_v + 512u, vrow + 512);
+  }
+  if (at.has_sc) copy16(dst + at.to_sc, kc + (off * NB + at.from_sc));
 }
-__device__ __forceinline__ void load_frag(Frag<2>& f, const uint8_t* kc, uint32_t off, const LaneOffsets<2>& at) {
-  const uint8_t *row = kc + off * 32u, *sc = kc + off * 2u;
-  f.k0 = ldg8(row + at.k);
-  f.k1 = ldg8(row + at.k + 256);
-  f.ks = ldg4(sc + at.ks);
-  f.vs = ldg8(sc + at.vs);
-  const uint8_t* v = row + at.v;
-  f.v[0] = ldg4(v);
-  f.v[1] = ldg4(v + 32);
-  f.v[2] = ldg4(v + 256);
-  f.v[3] = ldg4(v + 288);
+__device__ __forceinline__ void read_k(Frag<4>& f, uint32_t src, const GroupLane<4>& at) {
+  f.k0 = ld_shared_v4(src + at.k);
+  f.k1 = ld_shared_v4(src + at.k + 512u);
+  f.ks = ld_shared_v2(src + at.ks);
+}
+__device__ __forceinline__ void read_k(Frag<2>& f, uint32_t src, const GroupLane<2>& at) {
+  f.k0 = ld_shared_v2(src + at.k);
+  f.k1 = ld_shared_v2(src + at.k + 256u);
+  f.ks = ld_shared_u32(src + at.ks);
+}
+__device__ __forceinline__ void read_v(VFrag<4>& f, uint32_t src, const GroupLane<4>& at) {
+  f.vs = ld_shared_v4(src + at.vs);
+  f.v[0] = ld_shared_v2(src + at.v);
+  f.v[1] = ld_shared_v2(src + at.v + 64u);
+  f.v[2] = ld_shared_v2(src + at.v + 512u);
+  f.v[3] = ld_shared_v2(src + at.v + 576u);
+}
+__device__ __forceinline__ void read_v(VFrag<2>& f, uint32_t src, const GroupLane<2>& at) {
+  f.vs = ld_shared_v2(src + at.vs);
+  f.v[0] = ld_shared_u32(src + at.v);
+  f.v[1] = ld_shared_u32(src + at.v + 32u);
+  f.v[2] = ld_shared_u32(src + at.v + 256u);
+  f.v[3] = ld_shared_u32(src + at.v + 288u);
 }
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -115,7 +163,7 @@ __device__ __forceinline__ void k_scales(const Frag<2>& f, int b, float& s0, flo
 }
 
 // V scale bytes of the lane's keys (2c, 2c + 1) [h = 0] or (2c + 8, 2c + 9) [h = 1] as 16-bit pairs, block b.
-__device__ __forceinline__ void v_scale_pairs(const Frag<4>& f, uint32_t (&s)[4][2]) {
+__device__ __forceinline__ void v_scale_pairs(const VFrag<4>& f, uint32_t (&s)[4][2]) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const uint32_t a = h ? f.vs.z : f.vs.x, b = h ? f.vs.w : f.vs.y;
@@ -126,7 +174,7 @@ __device__ __forceinline__ void v_scale_pairs(const Frag<4>& f, uint32_t (&s)[4]
     s[3][h] = (hi >> 8) & 0x00FF00FFu;
   }
 }
-__device__ __forceinline__ void v_scale_pairs(const Frag<2>& f, uint32_t (&s)[2][2]) {
+__device__ __forceinline__ void v_scale_pairs(const VFrag<2>& f, uint32_t (&s)[2][2]) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const uint32_t a = h ? f.vs.y : f.vs.x;      // halves: keys 2c, 2c + 1; bytes: blocks 0, 1
@@ -138,17 +186,20 @@ __device__ __forceinline__ void v_scale_pairs(const Frag<2>& f, uint32_t (&s)[2]
 // Nonzero where a scale byte of the lane's four keys is not within [r - 14, r + 1], r the reference byte of
 // its block (packed in `top` as r + 1). The subtraction borrows only above the first byte that is out of
 // range, which itself shows (for bytes up to r + 240; larger ones are V values past 2^112).
-__device__ __forceinline__ uint32_t v_out_of_range(const Frag<4>& f, uint32_t top) {
+__device__ __forceinline__ uint32_t v_out_of_range(const VFrag<4>& f, uint32_t top) {
   return ((top - f.vs.x) | (top - f.vs.y) | (top - f.vs.z) | (top - f.vs.w)) & 0xF0F0F0F0u;
 }
-__device__ __forceinline__ uint32_t v_out_of_range(const Frag<2>& f, uint32_t top) {
+__device__ __forceinline__ uint32_t v_out_of_range(const VFrag<2>& f, uint32_t top) {
   return ((top - f.vs.x) | (top - f.vs.y)) & 0xF0F0F0F0u;      // two keys a word: `top` holds the two blocks twice
 }
 
 template <int D, int NT>
 __global__ void __launch_bounds__(kSmallWarps * 32, NT == 1 ? 4 : 2) paged_small_kernel(const PagedParams p, const SplitParams sp) {
   constexpr int NB = D / 32, kRows = 8 * NT, kPad = D + 4;
-  __shared__ float so[kSmallWarps][kRows][kPad];
+  // the warps' rings; at the end the warps' results take their place
+  constexpr uint32_t kRing = kRingGroups * kGroupBytes<NB>, kRingBytes = kSmallWarps * kRing, kOutBytes = kSmallWarps * kRows * kPad * 4u;
+  __shared__ __align__(128) uint8_t ring[kRingBytes > kOutBytes ? kRingBytes : kOutBytes];
+  float (*so)[kRows][kPad] = reinterpret_cast<float (*)[kRows][kPad]>(ring);
   __shared__ float sm[kSmallWarps][kRows], sl[kSmallWarps][kRows];
   const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3u;
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
@@ -220,9 +271,9 @@ __global__ void __launch_bounds__(kSmallWarps * 32, NT == 1 ? 4 : 2) paged_small
   const int32_t* table = p.block_table + static_cast<int64_t>(r) * p.table_width;
   const uint32_t n_pages = static_cast<uint32_t>(p.n_pages), page_mask = (1u << p.page_shift) - 1u;
   const uint32_t head_bytes = 2u * cache_chunk_bytes(D, 1u << p.page_shift);
-  const uint64_t page_bytes = static_cast<uint64_t>(p.Hkv) * head_bytes;
+  const uint32_t page_bytes = static_cast<uint32_t>(p.Hkv) * head_bytes;      // below 2^32 for every supported shape
+  const GroupLane<NB> at(lane, p.page_shift);
   const uint8_t* base = p.cache + static_cast<uint64_t>(head) * head_bytes;
-  const LaneOffsets<NB> at(lane, p.page_shift);
 
   // Scores stay in units of the columns' qscale: thr is the raw score that moves a reference, mu7 = m - 7
   // (0 while the column has seen no key, so that 2^(-inf - mu7) is 0 and not NaN).
@@ -245,12 +296,20 @@ __global__ void __launch_bounds__(kSmallWarps * 32, NT == 1 ? 4 : 2) paged_small
   auto page_of = [&](int grp) -> int {
     return grp < stop ? __ldg(table + ((grp << 4) >> p.page_shift)) : -1;     // looked at when it is used: a comparison would wait
   };
-  auto fetch = [&](Frag<NB>& f, int grp, int page) {
-    if (static_cast<uint32_t>(page) < n_pages)
-      load_frag(f, base + static_cast<uint32_t>(page) * page_bytes, (static_cast<uint32_t>(grp) << 4) & page_mask, at);
+  // The ring holds the next kRingGroups groups of this warp, copied asynchronously; their pages are looked up
+  // one turn before the copy. `there` remembers, newest group in bit 0, which of them have a page.
+  const uint32_t my_ring = smem_u32(ring) + warp * kRing;
+  uint32_t there = 0u;
+  auto fetch = [&](uint32_t dst, int grp, int page) {
+    const bool ok = static_cast<uint32_t>(page) < n_pages;
+    there = (there << 1) | (ok ? 1u : 0u);
+    if (ok) fetch_group<NB>(dst, lane, at, base + static_cast<uint64_t>(static_cast<uint32_t>(page)) * page_bytes, (static_cast<uint32_t>(grp) << 4) & page_mask);
+    copies_commit();
   };
-  auto step = [&](Frag<NB>& f, int grp) {
+  auto step = [&](uint32_t slot, int grp, auto&& refill) {
     const int key0 = grp << 4;
+    Frag<NB> f;
+    read_k(f, slot, at);
     // ---- S^T: partial scores of each 32-channel block, times the block's scale
     float s[NT][4];
 #pragma unroll
@@ -311,11 +370,14 @@ __global__ void __launch_bounds__(kSmallWarps * 32, NT == 1 ? 4 : 2) paged_small
       l[nt][1] += pv[nt][1] + pv[nt][3];
     }
     // ---- V's scales relative to the reference exponents
+    VFrag<NB> fv;
+    read_v(fv, slot, at);
+    refill();
     uint32_t vs[NB][2];
-    v_scale_pairs(f, vs);
+    v_scale_pairs(fv, vs);
     bool wide = false;
     const bool tail = key0 + 16 > lim_max;
-    if (__any_sync(0xffffffffu, v_out_of_range(f, rb_top) != 0u) || tail) {
+    if (__any_sync(0xffffffffu, v_out_of_range(fv, rb_top) != 0u) || tail) {
       // a scale above the reference moves it (O is scaled down); one far below takes the wide path
       rb_top = 0u;
 #pragma unroll
@@ -352,33 +414,30 @@ __global__ void __launch_bounds__(kSmallWarps * 32, NT == 1 ? 4 : 2) paged_small
       }
       if (NB == 2) rb_top |= rb_top << 16;
     }
-    // ---- P^T (key pairs of column g): fp16 in general, bf16 on the wide path
-    uint32_t pt[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      if (!wide) {
-        pt[nt][0] = transpose8x8(pack_half2(pv[nt][0], pv[nt][1]));
-        pt[nt][1] = transpose8x8(pack_half2(pv[nt][2], pv[nt][3]));
-      } else {
-        pt[nt][0] = transpose8x8(pack_bf162(pv[nt][0], pv[nt][1]));
-        pt[nt][1] = transpose8x8(pack_bf162(pv[nt][2], pv[nt][3]));
-      }
-    }
-    // ---- O^T += V^T P^T. Words w of a key pair hold blocks 2w, 2w + 1; nibbles of the two keys are
-    //      brought together so that one cvt gives the pair of one channel.
-#pragma unroll
-    for (int w = 0; w < NB / 2; ++w) {
-      uint32_t ev[2][4], od[2][4];            // [key pair][2 (block & 1) + tile]: rows g and g + 8
+    // ---- O^T += V^T P^T: P^T (key pairs of column g) by movmatrix. Words w of a key pair hold blocks 2w,
+    //      2w + 1; nibbles of the two keys are brought together so that one cvt gives the pair of one channel:
+    //      [key pair][2 (block & 1) + tile], rows g (even nibbles) and g + 8 (odd nibbles).
+    auto v_pairs = [&](int w, uint32_t (&ev)[2][4], uint32_t (&od)[2][4]) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const uint32_t x = word_of(f.v[2 * h], w), y = word_of(f.v[2 * h + 1], w);
+        const uint32_t x = word_of(fv.v[2 * h], w), y = word_of(fv.v[2 * h + 1], w);
         e2m1x8_to_half2((x & 0x0F0F0F0Fu) | ((y << 4) & 0xF0F0F0F0u), ev[h]);
         e2m1x8_to_half2(((x >> 4) & 0x0F0F0F0Fu) | (y & 0xF0F0F0F0u), od[h]);
       }
+    };
+    uint32_t pt[NT][2], ev[2][4], od[2][4];
+    if (!wide) {
 #pragma unroll
-      for (int bb = 0; bb < 2; ++bb) {
-        const int b = 2 * w + bb;
-        if (!wide) {
+      for (int nt = 0; nt < NT; ++nt) {
+        pt[nt][0] = transpose8x8(pack_half2(pv[nt][0], pv[nt][1]));
+        pt[nt][1] = transpose8x8(pack_half2(pv[nt][2], pv[nt][3]));
+      }
+#pragma unroll
+      for (int w = 0; w < NB / 2; ++w) {
+        v_pairs(w, ev, od);
+#pragma unroll
+        for (int bb = 0; bb < 2; ++bb) {
+          const int b = 2 * w + bb;
           const uint32_t sc0 = vs[b][0] * 1024u + sc_add[b], sc1 = vs[b][1] * 1024u + sc_add[b];   // 2^(s - r)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
@@ -387,8 +446,21 @@ __global__ void __launch_bounds__(kSmallWarps * 32, NT == 1 ? 4 : 2) paged_small
             for (int t = 0; t < 2; ++t)
               mma_f16(o[nt][2 * b + t], ev[0][2 * bb + t], od[0][2 * bb + t], ev[1][2 * bb + t], od[1][2 * bb + t], b0, b1);
           }
-        } else {
-          // bf16 V relative to the reference: code 2^(s - r), exact; P in bf16
+        }
+      }
+    } else {
+      // bf16 V relative to the reference, code 2^(s - r), exact; P in bf16
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        pt[nt][0] = transpose8x8(pack_bf162(pv[nt][0], pv[nt][1]));
+        pt[nt][1] = transpose8x8(pack_bf162(pv[nt][2], pv[nt][3]));
+      }
+#pragma unroll
+      for (int w = 0; w < NB / 2; ++w) {
+        v_pairs(w, ev, od);
+#pragma unroll
+        for (int bb = 0; bb < 2; ++bb) {
+          const int b = 2 * w + bb;
           uint32_t e2[2][2], o2[2][2];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -410,24 +482,32 @@ __global__ void __launch_bounds__(kSmallWarps * 32, NT == 1 ? 4 : 2) paged_small
       }
     }
   };
-  // one group ahead in registers (two sets that change roles), its page looked up one group earlier still
   int grp = first + static_cast<int>(warp);
-  int page = page_of(grp), page_next = page_of(grp + kSmallWarps);
-  Frag<NB> fa, fb;
-  fetch(fa, grp, page);
-  while (grp < stop) {
-    fetch(fb, grp + kSmallWarps, page_next);
-    int page_after = page_of(grp + 2 * kSmallWarps);
-    if (static_cast<uint32_t>(page) < n_pages) step(fa, grp);
-    grp += kSmallWarps;
-    if (grp >= stop) break;
-    page = page_after;
-    fetch(fa, grp + kSmallWarps, page);
-    page_after = page_of(grp + 2 * kSmallWarps);
-    if (static_cast<uint32_t>(page_next) < n_pages) step(fb, grp);
-    page_next = page_after;
-    grp += kSmallWarps;
+  {
+    int pages[kRingGroups];
+#pragma unroll
+    for (int i = 0; i < kRingGroups; ++i) pages[i] = page_of(grp + i * kSmallWarps);
+#pragma unroll
+    for (int i = 0; i < kRingGroups; ++i) fetch(my_ring + i * kGroupBytes<NB>, grp + i * kSmallWarps, pages[i]);
   }
+  int page_ahead = page_of(grp + kRingGroups * kSmallWarps);
+  uint32_t slot = my_ring;
+  for (; grp < stop; grp += kSmallWarps) {
+    copies_wait<kRingGroups - 1>();
+    __syncwarp();
+    const uint32_t now = slot;
+    slot = slot == my_ring + (kRingGroups - 1) * kGroupBytes<NB> ? my_ring : slot + kGroupBytes<NB>;
+    auto refill = [&]() {
+      __syncwarp();                           // the slot is read by every lane before it is filled again
+      fetch(now, grp + kRingGroups * kSmallWarps, page_ahead);
+      page_ahead = page_of(grp + (kRingGroups + 1) * kSmallWarps);
+    };
+    if ((there >> (kRingGroups - 1)) & 1u) step(now, grp, refill);
+    else refill();
+  }
+  copies_wait<0>();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  __syncthreads();                            // the rings give way to the results
 
   // ---- the warps' results meet in shared memory
 #pragma unroll
@@ -502,23 +582,40 @@ __global__ void __launch_bounds__(128) paged_combine_kernel(const PagedParams p,
   const RequestRange rq = request_range(p, r);
   const int used = static_cast<int>((rq.cap + sp.chunk - 1) / sp.chunk);
   if (i >= rq.n || used <= 1) return;
+  asm volatile("griddepcontrol.wait;" ::: "memory");      // launched ahead of the parts' end, see launch_rows
   const int64_t orow = static_cast<int64_t>(rq.start + i) * p.Hq + h;
   const float* lse = sp.part_lse + orow * sp.splits;
   const float* po = sp.part_o + orow * sp.splits * D + lane * kPer;
+  static_assert(kMaxSplits <= 128, "four splits a lane");
+  float w[4];                              // lane s % 32 has the weight of split s
   float top = -INFINITY;
-  for (int s = lane; s < used; s += 32) top = fmaxf(top, lse[s]);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    w[j] = lane + 32 * j < used ? lse[lane + 32 * j] : -INFINITY;
+    top = fmaxf(top, w[j]);
+  }
 #pragma unroll
   for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
   const float base = top == -INFINITY ? 0.f : top;
   float sum = 0.f, acc[kPer];
 #pragma unroll
-  for (int x = 0; x < kPer; ++x) acc[x] = 0.f;
-#pragma unroll 4
-  for (int s = 0; s < used; ++s) {
-    const float k = ex2(lse[s] - base);
-    sum += k;
+  for (int j = 0; j < 4; ++j) {
+    w[j] = ex2(w[j] - base);
+    sum += w[j];
+  }
 #pragma unroll
-    for (int x = 0; x < kPer; ++x) acc[x] = fmaf(k, po[static_cast<int64_t>(s) * D + x], acc[x]);
+  for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+#pragma unroll
+  for (int x = 0; x < kPer; ++x) acc[x] = 0.f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int n = min(used - 32 * j, 32);
+#pragma unroll 8
+    for (int s = 0; s < n; ++s) {
+      const float k = __shfl_sync(0xffffffffu, w[j], s);
+#pragma unroll
+      for (int x = 0; x < kPer; ++x) acc[x] = fmaf(k, po[static_cast<int64_t>(32 * j + s) * D + x], acc[x]);
+    }
   }
   const float inv = sum > 0.f ? 1.f / sum : 0.f;
 #pragma unroll
@@ -538,15 +635,20 @@ SplitPlan plan_splits(int64_t T, int R, int Hq, int Hkv, int d, int max_new, int
   const int64_t unit = s.tc ? 128 : 64;                      // chunks are multiples of this many keys
   s.row_tiles = (rows + per - 1) / per;
   const int64_t units = static_cast<int64_t>(R) * Hkv * s.row_tiles;
+  // A long batch is cut into this many CTAs: four for each of 148 x 4 places with one column tile, two for
+  // each of 148 x 2 with two (64 ragged requests of up to 8192 keys: 88 us, 99 with half as many; 2 x 131072
+  // keys and two column tiles: 115 us, 134 with twice or half as many).
+  constexpr int64_t kSpread[3] = {0, 2368, 592};
   int64_t chunk;
   if (s.tc) chunk = units >= 592 ? max_kv : (units * max_kv + 887) / 888;      // six CTAs for each SM, or four without splits
-  else chunk = (units * max_kv + 1183) / 1184;               // two CTAs for each of 148 x 4 places
+  else chunk = (units * max_kv + kSpread[s.nt] - 1) / kSpread[s.nt];
+
   if (s.tc && chunk < 1024) chunk = 1024;
   chunk = (chunk + unit - 1) / unit * unit;
   if (chunk < unit) chunk = unit;
   int64_t splits = (max_kv + chunk - 1) / chunk;
-  if (splits > 128) {
-    chunk = ((max_kv + 127) / 128 + unit - 1) / unit * unit;
+  if (splits > kMaxSplits) {
+    chunk = ((max_kv + kMaxSplits - 1) / kMaxSplits + unit - 1) / unit * unit;
     splits = (max_kv + chunk - 1) / chunk;
   }
   s.chunk = chunk;
@@ -568,8 +670,17 @@ static cudaError_t launch_rows(const PagedParams& p, const SplitParams& sp, cons
   }
   if (e != cudaSuccess || s.splits == 1) return e;
   const int64_t rows = static_cast<int64_t>(p.R) * p.max_new * p.Hq;
-  paged_combine_kernel<D><<<static_cast<unsigned>((rows + 3) / 4), 128, 0, stream>>>(p, sp);
-  return cudaGetLastError();
+  // started while the last parts are still being made: it looks up its rows and then waits for their end
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>((rows + 3) / 4));
+  cfg.blockDim = dim3(128);
+  cfg.stream = stream;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_combine_kernel<D>, p, sp);
 }
 
 cudaError_t launch_paged(const PagedParams& p, const SplitPlan& s, void* part, int d, cudaStream_t stream) {

@@ -523,6 +523,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const PagedPara
       if (lane == 0) mbar_arrive(&s.bar_p_full[x]);
     }
     // ---- out = O / l, or the split's part
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (ok && n > 0) ok = warp_wait_tc(&s.bar_pv[x], (n - 1) & 1, abort_flag, p.status, kStatusTimeoutPV | 4 | x);
     if (ok) {
       tc_fence_after();
