@@ -188,12 +188,12 @@ struct SplitPlan {
   int64_t row_tiles, chunk, splits, units;
   int64_t part_rows;       // partial rows in the workspace (0: one split)
 };
-SplitPlan plan_splits(int64_t T, int R, int Hq, int Hkv, int d, int max_new, int64_t max_kv);
+SplitPlan plan_splits(int R, int Hq, int Hkv, int d, int max_new, int64_t max_kv);
 struct SplitParams {
   int64_t chunk;           // keys of one split
   uint32_t splits, row_tiles;
-  float* part_o;           // [T, Hq, splits, d] normalised partial rows
-  float* part_lse;         // [T, Hq, splits] log2 of their sums
+  float* part_o;           // [R, max_new, Hq, splits, d] normalised partial rows
+  float* part_lse;         // [R, max_new, Hq, splits] log2 of their sums
 };
 cudaError_t launch_paged_tc(const PagedParams& p, const SplitParams& sp, int d, int64_t units, cudaStream_t stream);
 cudaError_t launch_paged(const PagedParams& p, const SplitPlan& s, void* part, int d, cudaStream_t stream);

@@ -31,7 +31,7 @@ mxattn_status check_cache(const void* cache, int Hkv, int d, int page_size, int6
 }
 
 // Status area, then the partial rows of split requests.
-size_t paged_workspace(int64_t T, const SplitPlan& s, int d) {
+size_t paged_workspace(const SplitPlan& s, int d) {
   return 256 + static_cast<size_t>(s.part_rows) * (d + 1) * sizeof(float);
 }
 
@@ -129,7 +129,7 @@ mxattn_status mxattn_cache_read(const uint8_t* cache, const int64_t* slots, int6
 
 size_t mxattn_paged_workspace_size(int64_t T, int R, int Hq, int Hkv, int d, int max_new, int64_t max_kv) {
   if (T < 0 || R < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || (d != 64 && d != 128) || max_new < 0 || max_kv < 0) return 0;
-  return paged_workspace(T, plan_splits(T, R, Hq, Hkv, d, max_new, max_kv), d);
+  return paged_workspace(plan_splits(R, Hq, Hkv, d, max_new, max_kv), d);
 }
 
 mxattn_status mxattn_paged_forward(const void* q, int64_t q_token_stride, int64_t q_head_stride, const uint8_t* cache,
@@ -147,9 +147,9 @@ mxattn_status mxattn_paged_forward(const void* q, int64_t q_token_stride, int64_
   if (!workspace || !aligned(workspace, 256)) return MXATTN_ERR_INVALID_ARG;
   if (static_cast<int64_t>(max_new) * (Hq / Hkv) >= (1ll << 30) || static_cast<int64_t>(max_new) * Hq >= (1ll << 31) / (R > 0 ? R : 1))
     return MXATTN_ERR_UNSUPPORTED;
-  const SplitPlan plan = plan_splits(T, R, Hq, Hkv, d, max_new, max_kv);
+  const SplitPlan plan = plan_splits(R, Hq, Hkv, d, max_new, max_kv);
   if (plan.units >= (1ll << 31)) return MXATTN_ERR_UNSUPPORTED;
-  if (workspace_bytes < paged_workspace(T, plan, d)) return MXATTN_ERR_WORKSPACE;
+  if (workspace_bytes < paged_workspace(plan, d)) return MXATTN_ERR_WORKSPACE;
   if (T == 0 || R == 0 || max_new == 0) return MXATTN_OK;
   if (!q || !out || !q_start || !kv_len || (table_width > 0 && !block_table)) return MXATTN_ERR_INVALID_ARG;
   if (!aligned(q, 16) || q_token_stride % 8 != 0 || q_head_stride % 8 != 0 || !aligned(out, 16) || !aligned(lse, 4) ||

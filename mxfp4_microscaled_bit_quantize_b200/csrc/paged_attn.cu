@@ -560,10 +560,11 @@ __global__ void __launch_bounds__(kSmallWarps * 32, NT == 1 ? 4 : 2) paged_small
         *reinterpret_cast<uint32_t*>(p.out + orow * D + lane * kPer + x) = pack_bf162(acc[x] * inv, acc[x + 1] * inv);
       if (p.lse && lane == 0) p.lse[orow] = lse2 * 0.6931471805599453f;
     } else {
-      float* po = sp.part_o + (orow * sp.splits + split) * D + lane * kPer;
+      const int64_t prow = ((static_cast<int64_t>(r) * p.max_new + i) * p.Hq + head * G + h) * sp.splits + split;
+      float* po = sp.part_o + prow * D + lane * kPer;
 #pragma unroll
       for (int x = 0; x < kPer; ++x) po[x] = acc[x] * inv;
-      if (lane == 0) sp.part_lse[orow * sp.splits + split] = lse2;
+      if (lane == 0) sp.part_lse[prow] = lse2;
     }
   }
 }
@@ -584,8 +585,9 @@ __global__ void __launch_bounds__(128) paged_combine_kernel(const PagedParams p,
   if (i >= rq.n || used <= 1) return;
   asm volatile("griddepcontrol.wait;" ::: "memory");      // launched ahead of the parts' end, see launch_rows
   const int64_t orow = static_cast<int64_t>(rq.start + i) * p.Hq + h;
-  const float* lse = sp.part_lse + orow * sp.splits;
-  const float* po = sp.part_o + orow * sp.splits * D + lane * kPer;
+  const int64_t prow = ((static_cast<int64_t>(r) * p.max_new + i) * p.Hq + h) * sp.splits;
+  const float* lse = sp.part_lse + prow;
+  const float* po = sp.part_o + prow * D + lane * kPer;
   static_assert(kMaxSplits <= 128, "four splits a lane");
   float w[4];                              // lane s % 32 has the weight of split s
   float top = -INFINITY;
@@ -626,7 +628,7 @@ __global__ void __launch_bounds__(128) paged_combine_kernel(const PagedParams p,
 
 // Up to 16 rows (new tokens x heads of a group) go to the mma.sync kernel, whose time does not depend on
 // rows that are not there; more rows share the tcgen05 kernel's conversion of the keys.
-SplitPlan plan_splits(int64_t T, int R, int Hq, int Hkv, int d, int max_new, int64_t max_kv) {
+SplitPlan plan_splits(int R, int Hq, int Hkv, int d, int max_new, int64_t max_kv) {
   SplitPlan s{};
   const int64_t rows = static_cast<int64_t>(max_new) * (Hq / Hkv);
   s.tc = rows > 16;
@@ -654,7 +656,7 @@ SplitPlan plan_splits(int64_t T, int R, int Hq, int Hkv, int d, int max_new, int
   s.chunk = chunk;
   s.splits = splits < 1 ? 1 : splits;
   s.units = units * s.splits;
-  s.part_rows = s.splits > 1 ? T * Hq * s.splits : 0;
+  s.part_rows = s.splits > 1 ? static_cast<int64_t>(R) * max_new * Hq * s.splits : 0;   // at most about 890 x 256
   return s;
 }
 

@@ -531,7 +531,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const PagedPara
       sum += __shfl_xor_sync(0xffffffffu, sum, 16);
       const float inv = sum > 0.f ? 1.f / sum : 0.f;
       const float lse2 = sum > 0.f ? mu + log2f(sum) : -INFINITY;
-      const int64_t orow = static_cast<int64_t>(rq.start + i) * p.Hq + head * G + h;
+      int64_t orow = static_cast<int64_t>(rq.start + i) * p.Hq + head * G + h;
       const uint32_t live_rows = __popc(__ballot_sync(0xffffffffu, live) & 0xFFFFu);   // the warp's first rows
       // The rows leave through shared memory (Q's, which no product reads any more), so that a store
       // instruction covers whole lines: passes of up to 256 bytes of each of the warp's 16 rows, piece j
@@ -542,14 +542,18 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const PagedPara
       auto flush = [&](uint32_t pieces, uint8_t* dst, int64_t row_bytes) {    // pieces of 16 bytes per row: 8 or 16
         __syncwarp();
         const uint32_t per = 32u / pieces, pc = static_cast<uint32_t>(lane) % pieces;
-        for (uint32_t rr0 = 0; rr0 < live_rows; rr0 += per) {
+#pragma unroll 4
+        for (uint32_t rr0 = 0; rr0 < 16u; rr0 += per) {
           const uint32_t rr = rr0 + static_cast<uint32_t>(lane) / pieces;
-          const int64_t to = __shfl_sync(0xffffffffu, orow, rr & 15u);
-          if (rr < live_rows) *reinterpret_cast<uint4*>(dst + to * row_bytes + pc * 16u) = ld_shared_v4(stage + rr * 256u + ((pc ^ (rr & 7u)) << 4));
+          const int64_t to = __shfl_sync(0xffffffffu, orow, rr);
+          const uint4 val = ld_shared_v4(stage + rr * 256u + ((pc ^ (rr & 7u)) << 4));
+          if (rr < live_rows) *reinterpret_cast<uint4*>(dst + to * row_bytes + pc * 16u) = val;
         }
         __syncwarp();
       };
       const bool direct = used_splits == 1;
+      // parts are indexed by request and token, which bounds them by what the plan laid out
+      if (!direct) orow = (static_cast<int64_t>(r) * p.max_new + i) * p.Hq + head * G + h;
       // fp32 parts: 64 channels a pass; with d = 128 a pass takes one half of the lanes' channels
       const int passes = direct ? 1 : D / 64;
 #pragma unroll 1

@@ -85,6 +85,9 @@ def test_paged_refusals(lib, change, status):
 
 def test_paged_workspace_size(lib):
     assert lib.mxattn_paged_workspace_size(64, 64, 32, 8, 128, 1, 8192) >= 256
+    # it follows the requests, not the rows of a padded batch
+    assert lib.mxattn_paged_workspace_size(1 << 20, 4, 32, 8, 128, 1, 131072) == lib.mxattn_paged_workspace_size(4, 4, 32, 8, 128, 1, 131072) < 64 << 20
+    assert lib.mxattn_paged_workspace_size(4096, 1, 32, 8, 128, 4096, 131072) < 256 << 20
     for bad in ((-1, 1, 4, 2, 128, 1, 9), (1, -1, 4, 2, 128, 1, 9), (1, 1, 3, 2, 128, 1, 9), (1, 1, 4, 2, 96, 1, 9), (1, 1, 4, 2, 128, -1, 9),
                 (1, 1, 4, 2, 128, 1, -9), (1, 1, 4, 0, 128, 1, 9)):
         assert lib.mxattn_paged_workspace_size(*bad) == 0
