@@ -346,11 +346,13 @@ mxattn_status mxattn_cache_read(const uint8_t* cache, const int64_t* slots, int6
  *   n attends to keys j <= kv_len - n + i (causal = 1), or to all j < kv_len (causal = 0: cross
  *   attention to cached states of any other length). Scores and sums are fp32, Q is not quantized,
  *   the probabilities enter their product with 8 significant bits or more.
- *   A row with no key gets out = 0. Rows of no request are left as they were.
+ *   A row with no key gets out = 0. Rows of no request are left as they were. out must not overlap q.
  *   max_new, max_kv: upper bounds of the requests' new tokens and of kv_len, from which the work is
  *   laid out; rows of a request past max_new are left as they were, keys past max_kv or past
  *   table_width pages are not attended to. Table entries outside [0, n_pages) count as no keys.
- *   q_start values are clamped to [0, T], a negative kv_len counts as 0.
+ *   q_start values are clamped to [0, T], a negative kv_len counts as 0. Ranges of two requests must
+ *   not overlap. Supported: max_new * Hq / Hkv < 2^30, R * max_new * Hq < 2^31.
+ *   Two launches at most (the second joins the parts of split contexts), deterministic.
  *   workspace: mxattn_paged_workspace_size(...) bytes, 256-byte aligned, contents on entry ignored,
  *   not used concurrently by another call; its first word is the status word of
  *   mxattn_check_status. A call with T, R or max_new 0 does nothing and leaves it as it was.

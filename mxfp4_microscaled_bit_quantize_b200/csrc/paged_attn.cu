@@ -2,26 +2,34 @@
 //
 //   x_j = (q . k_j) log2(e) / sqrt(d),  out = sum_j 2^(x_j - m) v_j / sum_j 2^(x_j - m)
 //
-// Bound: 17/16 d bytes of K and V per key and KV head have to come from HBM once, for all query heads
-// of the group and all new tokens; at 6.5 TB/s an SM may spend about 90 clocks on 16 keys of d = 128.
-// So the kernel keeps the instructions per key down rather than the FLOPs:
-//   * a warp takes 16 keys at a time straight from global memory into mma fragments (the cache's
-//     layout does the gather, see cache_layout.cuh), one group ahead of the one it works on; the
-//     four warps of a CTA take turns on the groups and meet once, at the end;
-//   * S^T = K Q^T and O^T += V^T P^T with mma.m16n8k16: the keys (or channels) are the 16 rows, the
-//     queries (tokens x heads of the group) the 8 columns, so that decoding wastes no half tile;
-//   * E2M1 codes become fp16 by cvt (exact, 64 codes pairs per clock and SM); no scale is ever
-//     multiplied into K or V: a K block's scale multiplies its 32-channel partial score in fp32, a V
-//     block's scale its fp16 probability, four multiplications each for 8 queries instead of 16;
-//   * Q is fp16 after a power of two per row that brings its largest element to [2^7, 2^8) (bf16's 8
-//     bits fit, elements 2^-21 below the largest and smaller lose bits below 2^-32 of it);
-//   * the reference m of a column moves only when a score passes it by 7, so that the maximum over
-//     the warp's lanes is rarely taken; p = 2^(x - m + 7) <= 2^14 is summed in fp32 and rounded to
-//     fp16 (11 bits) for the product;
-//   * V's block scales enter relative to r_b, the largest exponent so far of channel block b, as
-//     2^(s - r_b) in fp16. A group with a block more than 14 binades below r_b takes a slower path
-//     with bf16 operands, whose range needs no such care.
-// A long context is split over CTAs (chunk keys each); their results meet in combine_kernel.
+// Bound: 17/16 d bytes of K and V per key and KV head have to come from HBM once, for all query heads of the
+// group and all new tokens. At 6.5 TB/s an SM may spend about 90 clocks on 16 keys of d = 128, and E2M1 codes
+// have to become numbers in that time, so the kernel keeps the instructions per key down rather than the FLOPs:
+//   * a warp takes 16 keys at a time in the order of the mma fragments (the cache's layout does the gather, see
+//     cache_layout.cuh) from a ring of its own in shared memory, into which it copies four groups ahead; the four
+//     warps of a CTA take turns on the groups and meet once, at the end;
+//   * S^T = K Q^T and O^T += V^T P^T with mma.m16n8k16: the keys (or channels) are the 16 rows, the queries
+//     (tokens x heads of the group) the 8 columns, so that decoding wastes no half tile. tcgen05's smallest tile
+//     has 128 rows; here there are up to 16;
+//   * E2M1 codes become fp16 by cvt (exact); no scale is ever multiplied into K or V: a K block's scale
+//     multiplies its 32-channel partial score in fp32, a V block's scale its fp16 probability, four
+//     multiplications each for 8 queries instead of 16;
+//   * Q is fp16 after a power of two per row that brings its largest element to [2^7, 2^8) (bf16's 8 bits fit,
+//     elements 2^-21 below the largest and smaller lose bits below 2^-32 of it);
+//   * the reference m of a column moves only when a score passes it by 7, so that the maximum over the warp's
+//     lanes is rarely taken; p = 2^(x - m + 7) <= 2^14 is summed in fp32 and rounded to fp16 (11 bits) for the
+//     product;
+//   * V's block scales enter relative to r_b, the largest exponent so far of channel block b, as 2^(s - r_b) in
+//     fp16. A group with a block more than 14 binades below r_b takes a slower path with bf16 operands, whose
+//     range needs no such care.
+// A long context is split over CTAs (chunk keys each); their results meet in paged_combine_kernel.
+//
+// Measured (d = 128, 32 query and 8 KV heads, pages of 16): 64 requests of up to 8192 keys, one token each, 86 us
+// (267 MB: 3.1 TB/s, 47 % of the copy bandwidth); 2 x 131072 keys, four tokens each, pages of 64: 112 us (285 MB:
+// 2.5 TB/s). The copies alone take 56 us of the 86; the rest is arithmetic that they do not hide: the ALU pipe,
+// which cvt shares with the logic on nibbles and scale bytes, is 56 % busy, the schedulers issue 64 % of the time
+// with 16 warps of 128 registers. Fragments loaded to registers one group ahead instead of the ring took 94 us, two
+// groups a turn, deeper rings or 12 warps of 168 registers the same as now.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cmath>

@@ -1,25 +1,33 @@
-// Attention of many new tokens over the paged MXFP4 KV cache (chunks of prompts, cross attention):
-// tcgen05 products in bf16 with K and V tiles made from the pages on the way to shared memory.
+// Attention of many new tokens over the paged MXFP4 KV cache (chunks of prompts, cross attention): tcgen05
+// products in bf16 with K and V tiles made from the pages on the way to shared memory.
 //
 //   S = Q K^T;  m' = max(m, rowmax S c),  c = log2(e) / sqrt(d);  P = 2^(S c - m');
 //   O = 2^(m - m') O + P V;  l = 2^(m - m') l + rowsum P;  out = O / l
 //
-// Bound: 4 d FLOP per (query head, key) on the tensor cores, next to one exponential (MUFU: 16 per
-// clock and SM) per (query head, key): for d = 128 and 256 query rows both need about 2100 clocks per
-// 128 keys. The conversion of the 128 keys (E2M1 times a power of two is exact in bf16) costs about
-// 800 issue slots per SM sub-partition, so a CTA owns 256 query rows to share it.
+// Bound: 4 d FLOP per (query head, key) on the tensor cores, next to one exponential (MUFU: 16 per clock and SM)
+// per (query head, key): for d = 128 and 256 query rows both need about 2100 clocks per 128 keys. The conversion
+// of the 128 keys (E2M1 times a power of two is exact in bf16) costs about 1000 issue slots per SM sub-partition,
+// half of them on the half-rate ALU pipe, so a CTA owns 256 query rows to share it.
 //
-// Work unit: one CTA (one per SM: it takes all 512 TMEM columns) owns 256 consecutive rows (token,
-// query head of the group) of one request and KV head, as two tiles A and B of 128, and visits the
-// keys of one split in tiles of 128. 512 threads:
-//   warps 0, 1   issue the products of tile A, B (one thread each): S(t) into TMEM, then P V(t) with P
-//                as the TMEM operand, then S(t + 1) over the same columns, each after the commit of the
-//                one before; the two tiles' products fill each other's gaps
-//   warps 4-7    convert: page lookups and code loads one tile ahead in registers, then K(t) and V(t)
-//                as bf16 into a two-stage ring (128-byte swizzle: K is K-major, V MN-major)
-//   warps 8-15   softmax of tiles A and B, one thread per row; O is rescaled in TMEM only when a row's
-//                maximum passes its reference by 8 (P <= 2^8 is bf16's business as usual)
+// Work unit: one CTA (one per SM: it takes all 512 TMEM columns) owns 256 consecutive rows (token, query head of
+// the group) of one request and KV head, as two tiles A and B of 128, and visits the keys of one split in tiles
+// of 128. 896 threads:
+//   warps 0, 1    issue the products of tile A, B (one thread each): S(t) into TMEM, then P V(t) with P as the
+//                 TMEM operand, then S(t + 1) over the same columns, each after the commit of the one before
+//   warps 4-11    convert: page lookups and code loads one tile ahead in registers, then K(t) and V(t) as bf16
+//                 into a two-stage ring (128-byte swizzle: K is K-major, V MN-major)
+//   warps 12-27   softmax of tiles A and B, two threads per row; the tiles' exponentials take turns, so that one
+//                 tile's products run under the other's; O is rescaled in TMEM only when a row's maximum passes
+//                 its reference by 8
 // P is rounded to bf16 (8 bits) for the product, the row sum is taken before the rounding, in fp32.
+//
+// Measured (d = 128): 2048 tokens over 30720 keys, 32 query and 8 KV heads: 1.28 ms, 833 TFLOP/s, 60 % of the
+// bf16 rate sustained under the power limit; 32760 rows x 40 heads over 512 keys: 0.72 ms, 477 TFLOP/s (four key
+// tiles per CTA: set-up, first loads and output are half of its 20 us). A pair of tiles takes about 4300 clocks
+// per 128 keys: a row tile's own chain (load S and maxima 900, exponentials 1500, hand-over 350, P V 650, S 1050)
+// is what bounds it. Tried and slower: one S buffer for both tiles with P in columns of its own, 64-key steps
+// with two S buffers a tile (M = 128, N = 64 products take as long as N = 128), fp16 tiles with the codes
+// converted by cvt (half the conversion, but a softmax that spills), several pairs of row tiles per CTA.
 #include <cuda_bf16.h>
 #include <cstdint>
 
