@@ -44,6 +44,7 @@ constexpr int kConvWarp0 = 4, kRowWarp0 = 12;    // warps 0-3 issue, 4-11 conver
 constexpr uint32_t kTcCols = 512, kColSx = 0, kColOx = 256;   // S / P of tile X at 128 X, O at 256 + 128 X
 constexpr uint32_t kSw128 = 2;                                // descriptor code of the 128-byte swizzle
 constexpr int kTcStages = 2;
+constexpr uint32_t kPlaces = 148;                             // CTAs that run at the same time, one per SM
 // A row's reference moves when a score passes it by this much (in powers of two). bf16 has fp32's range, so a
 // larger step would be safe, but a key that dominates its row enters without a rounding only while it is the
 // reference (P = 1): with 32 the error against 64 bits was 1.7 times that of fp32 arithmetic rounded once,
@@ -446,6 +447,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const PagedPara
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&s.bar_q);
+    // the Q rows of a CTA that will run when this one's place is free, on their way to L2
+    uint32_t nu = blockIdx.x + kPlaces;
+    if (nu < gridDim.x) {
+      nu /= sp.splits;
+      const int next_row = static_cast<int>(sp.row_tiles - 1 - nu % sp.row_tiles) * 256 + x * 128 + in_tile;
+      nu /= sp.row_tiles;
+      if (static_cast<int>(nu / p.Hkv) == r && next_row < rows_all) {
+        const __nv_bfloat16* next = p.q + (rq.start + next_row / G) * p.q_token_stride + (static_cast<int>(nu % p.Hkv) * G + next_row % G) * p.q_head_stride;
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(next + kh * (D / 2)));
+      }
+    }
 
     const uint32_t lane_addr = static_cast<uint32_t>(r0) << 16;
     const uint32_t t_s = tmem + lane_addr + kColSx + 128 * x, t_o = tmem + lane_addr + kColOx + 128 * x;
