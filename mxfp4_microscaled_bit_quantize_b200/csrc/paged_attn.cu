@@ -224,11 +224,47 @@ __global__ void __launch_bounds__(kSmallWarps * 32, NT == 1 ? 4 : 2) paged_small
   const int used_splits = max(1, static_cast<int>((rq.cap + sp.chunk - 1) / sp.chunk));
   if (rt * kRows >= n_used * G || split >= used_splits) return;
 
+  // ---- which keys: the copies go out before anything else is loaded
+  auto limit_of = [&](int i) -> int {        // keys j < limit are visible to token i (it grows with i)
+    return static_cast<int>(max(min(p.causal ? rq.kv - rq.n + i + 1 : rq.kv, rq.cap), static_cast<int64_t>(0)));
+  };
+  const int lim_min = limit_of(rt * kRows / G), lim_max = limit_of((min((rt + 1) * kRows, n_used * G) - 1) / G);
+  const int first = static_cast<int>(split * sp.chunk) >> 4;
+  const int stop = (min(lim_max, static_cast<int>(min((split + 1) * sp.chunk, static_cast<int64_t>(0x7FFFFFFF)))) + 15) >> 4;
+  const int32_t* table = p.block_table + static_cast<int64_t>(r) * p.table_width;
+  const uint32_t n_pages = static_cast<uint32_t>(p.n_pages), page_mask = (1u << p.page_shift) - 1u;
+  const uint32_t head_bytes = 2u * cache_chunk_bytes(D, 1u << p.page_shift);
+  const uint32_t page_bytes = static_cast<uint32_t>(p.Hkv) * head_bytes;      // below 2^32 for every supported shape
+  const GroupLane<NB> at(lane, p.page_shift);
+  const uint8_t* base = p.cache + static_cast<uint64_t>(head) * head_bytes;
+
+  auto page_of = [&](int grp) -> int {
+    return grp < stop ? __ldg(table + ((grp << 4) >> p.page_shift)) : -1;     // looked at when it is used: a comparison would wait
+  };
+  // The ring holds the next kRingGroups groups of this warp, copied asynchronously; their pages are looked up
+  // one turn before the copy. `there` remembers, newest group in bit 0, which of them have a page.
+  const uint32_t my_ring = smem_u32(ring) + warp * kRing;
+  uint32_t there = 0u;
+  auto fetch = [&](uint32_t dst, int grp, int page) {
+    const bool ok = static_cast<uint32_t>(page) < n_pages;
+    there = (there << 1) | (ok ? 1u : 0u);
+    if (ok) fetch_group<NB>(dst, lane, at, base + static_cast<uint64_t>(static_cast<uint32_t>(page)) * page_bytes, (static_cast<uint32_t>(grp) << 4) & page_mask);
+    copies_commit();
+  };
+  int grp = first + static_cast<int>(warp);
+  {
+    int pages[kRingGroups];
+#pragma unroll
+    for (int i = 0; i < kRingGroups; ++i) pages[i] = page_of(grp + i * kSmallWarps);
+#pragma unroll
+    for (int i = 0; i < kRingGroups; ++i) fetch(my_ring + i * kGroupBytes<NB>, grp + i * kSmallWarps, pages[i]);
+  }
+  int page_ahead = page_of(grp + kRingGroups * kSmallWarps);
+
   // ---- Q: column nt * 8 + g of this lane, channels 32 b + 8 c .. + 7 as four fp16 pairs
   uint32_t qf[NT][NB][4];
   float qscale[NT][2];
   int lim[NT][2];          // keys j < lim are visible to columns 2c, 2c + 1
-  int lim_max = 0, lim_min = 0x7FFFFFFF;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     const int row = rt * kRows + nt * 8 + static_cast<int>(g);
@@ -258,30 +294,15 @@ __global__ void __launch_bounds__(kSmallWarps * 32, NT == 1 ? 4 : 2) paged_small
         const uint32_t x = word_of(raw[b], w);
         qf[nt][b][w] = pack_half2(__uint_as_float(x << 16) * mul, __uint_as_float(x & 0xFFFF0000u) * mul);
       }
-    int64_t l64 = p.causal ? rq.kv - rq.n + i + 1 : rq.kv;
-    l64 = live ? max(min(l64, rq.cap), static_cast<int64_t>(0)) : 0;
-    const int mine = static_cast<int>(l64);
+    const int mine = live ? limit_of(i) : 0;
     const float back = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(e - 7 + 127) << 23);
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       const int from = (2 * c + x) * 4;
       qscale[nt][x] = __shfl_sync(0xffffffffu, back, from);
       lim[nt][x] = __shfl_sync(0xffffffffu, mine, from);
-      lim_max = max(lim_max, lim[nt][x]);
-      lim_min = min(lim_min, __shfl_sync(0xffffffffu, live ? 1 : 0, from) ? lim[nt][x] : 0x7FFFFFFF);
     }
   }
-  lim_max = __reduce_max_sync(0xffffffffu, lim_max);
-  lim_min = __reduce_min_sync(0xffffffffu, lim_min);
-
-  const int first = static_cast<int>(split * sp.chunk) >> 4;
-  const int stop = (min(lim_max, static_cast<int>(min((split + 1) * sp.chunk, static_cast<int64_t>(0x7FFFFFFF)))) + 15) >> 4;
-  const int32_t* table = p.block_table + static_cast<int64_t>(r) * p.table_width;
-  const uint32_t n_pages = static_cast<uint32_t>(p.n_pages), page_mask = (1u << p.page_shift) - 1u;
-  const uint32_t head_bytes = 2u * cache_chunk_bytes(D, 1u << p.page_shift);
-  const uint32_t page_bytes = static_cast<uint32_t>(p.Hkv) * head_bytes;      // below 2^32 for every supported shape
-  const GroupLane<NB> at(lane, p.page_shift);
-  const uint8_t* base = p.cache + static_cast<uint64_t>(head) * head_bytes;
 
   // Scores stay in units of the columns' qscale: thr is the raw score that moves a reference, mu7 = m - 7
   // (0 while the column has seen no key, so that 2^(-inf - mu7) is 0 and not NaN).
@@ -301,19 +322,6 @@ __global__ void __launch_bounds__(kSmallWarps * 32, NT == 1 ? 4 : 2) paged_small
 #pragma unroll
   for (int b = 0; b < NB; ++b) { rb[b] = -1; sc_add[b] = 0x04000400u * 16u; }
 
-  auto page_of = [&](int grp) -> int {
-    return grp < stop ? __ldg(table + ((grp << 4) >> p.page_shift)) : -1;     // looked at when it is used: a comparison would wait
-  };
-  // The ring holds the next kRingGroups groups of this warp, copied asynchronously; their pages are looked up
-  // one turn before the copy. `there` remembers, newest group in bit 0, which of them have a page.
-  const uint32_t my_ring = smem_u32(ring) + warp * kRing;
-  uint32_t there = 0u;
-  auto fetch = [&](uint32_t dst, int grp, int page) {
-    const bool ok = static_cast<uint32_t>(page) < n_pages;
-    there = (there << 1) | (ok ? 1u : 0u);
-    if (ok) fetch_group<NB>(dst, lane, at, base + static_cast<uint64_t>(static_cast<uint32_t>(page)) * page_bytes, (static_cast<uint32_t>(grp) << 4) & page_mask);
-    copies_commit();
-  };
   auto step = [&](uint32_t slot, int grp, auto&& refill) {
     const int key0 = grp << 4;
     Frag<NB> f;
@@ -490,15 +498,6 @@ __global__ void __launch_bounds__(kSmallWarps * 32, NT == 1 ? 4 : 2) paged_small
       }
     }
   };
-  int grp = first + static_cast<int>(warp);
-  {
-    int pages[kRingGroups];
-#pragma unroll
-    for (int i = 0; i < kRingGroups; ++i) pages[i] = page_of(grp + i * kSmallWarps);
-#pragma unroll
-    for (int i = 0; i < kRingGroups; ++i) fetch(my_ring + i * kGroupBytes<NB>, grp + i * kSmallWarps, pages[i]);
-  }
-  int page_ahead = page_of(grp + kRingGroups * kSmallWarps);
   uint32_t slot = my_ring;
   for (; grp < stop; grp += kSmallWarps) {
     copies_wait<kRingGroups - 1>();
