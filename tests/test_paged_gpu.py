@@ -381,6 +381,90 @@ def test_paged_on_another_stream(dev):
     _close(out, None, op.attention(*host, True), on[0], host[1])
 
 
+@pytest.mark.parametrize("n,Hq,H", [(1, 64, 1), (2, 24, 1), (5, 33, 3)])
+def test_paged_large_groups(dev, n, Hq, H):
+    # 64, 48 and 55 rows a KV head: few tokens, but more rows than the small kernel takes
+    on, host = make(dev, [(200, n), (17, n), (0, n)], True, Hq, H, 128, 32, seed=Hq)
+    _close(api.mxattn_paged_forward(*on, max_new=n), None, op.attention(*host, True), on[0], host[1])
+
+
+@pytest.mark.parametrize("n", [1, 60])
+def test_paged_two_calls_at_once(dev, n):
+    # two streams, a workspace each: the same bits as one after the other
+    calls = [make(dev, [(1500, n), (90, n)], True, 8, 2, 128, 16, seed=s, garbage=False, tail=0)[0] for s in (1, 2)]
+    want = [api.mxattn_paged_forward(*on, max_new=n) for on in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(dev) for _ in calls]
+    got = []
+    for st, on in zip(streams, calls):
+        with torch.cuda.stream(st):
+            got.append([api.mxattn_paged_forward(*on, max_new=n) for _ in range(8)])
+    torch.cuda.synchronize()
+    for outs, w in zip(got, want):
+        assert all(torch.equal(o, w) for o in outs)
+
+
+def test_empty_calls(dev):
+    cache = api.cache_alloc(3, 2, 64, 16, dev)
+    none = torch.empty(0, 2, 64, dtype=torch.bfloat16, device=dev)
+    slots = torch.empty(0, dtype=torch.int64, device=dev)
+    api.mxattn_cache_append(none, none, slots, cache)
+    assert api.mxattn_cache_read(cache, slots)[0].shape == (0, 2, 64)
+    table = torch.zeros(0, 4, dtype=torch.int32, device=dev)
+    start, kv, sl, info = api.mxattn_cache_plan(i32([], dev), i32([], dev), table, i32([1], dev), 16, 0)
+    assert start.tolist() == [0] and info.tolist() == [0, 0, 0, 0] and sl.numel() == 0
+    assert api.mxattn_paged_forward(none, cache, table, start, kv, max_new=0).shape == (0, 2, 64)
+    # a pool without pages and a table without columns: no keys, zeros
+    q = torch.ones(3, 4, 64, dtype=torch.bfloat16, device=dev)
+    for n in (1, 3):
+        for c, tab in ((cache[:0], torch.zeros(1, 4, dtype=torch.int32, device=dev)), (cache, torch.zeros(1, 0, dtype=torch.int32, device=dev))):
+            out = api.mxattn_paged_forward(q[:n], c, tab, i32([0, n], dev), i32([40], dev), max_new=n)
+            assert torch.all(out == 0)
+
+
+def test_captured_step_for_changing_batches(dev):
+    # plan, append and attend captured once with padded rows, replayed for batches that change on the device
+    H, Hq, d, P, width, T = 2, 8, 64, 16, 8, 6
+    rng = np.random.default_rng(3)
+    cache = api.cache_alloc(30, H, d, P, dev)
+    ctx, new = torch.zeros(3, dtype=torch.int32, device=dev), torch.ones(3, dtype=torch.int32, device=dev)
+    table = torch.full((3, width), -1, dtype=torch.int32, device=dev)
+    free = i32(rng.permutation(30), dev)
+    outs = (torch.zeros(4, dtype=torch.int32, device=dev), torch.zeros(3, dtype=torch.int32, device=dev),
+            torch.zeros(T, dtype=torch.int64, device=dev), torch.zeros(4, dtype=torch.int32, device=dev))
+    qkv = torch.zeros(T, Hq + 2 * H, d, dtype=torch.bfloat16, device=dev)
+    out = torch.zeros(T, Hq, d, dtype=torch.bfloat16, device=dev)
+    ws = torch.empty(api.paged_workspace_size(T, 3, Hq, H, d, 2, width * P), dtype=torch.uint8, device=dev)
+
+    def step():
+        api.mxattn_cache_plan(ctx, new, table, free, P, T, out=outs)
+        api.mxattn_cache_append(qkv[:, Hq:Hq + H], qkv[:, Hq + H:], outs[2], cache)
+        api.mxattn_paged_forward(qkv[:, :Hq], cache, table, outs[0], outs[1], max_new=2, max_kv=width * P, workspace=ws, out=out)
+
+    step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    cache.zero_()
+    table.fill_(-1)
+    host, host_table, pages, lens = np.zeros(tuple(cache.shape), dtype=np.uint8), np.full((3, width), -1), rng.permutation(30), [0, 0, 0]
+    for n in ([2, 1, 2], [1, 0, 2], [2, 2, 2], [0, 1, 0]) * 5:
+        ctx.copy_(i32(lens, dev))
+        new.copy_(i32(n, dev))
+        free.copy_(i32(np.concatenate([pages, np.full(30 - len(pages), -1)]), dev))
+        x = torch.from_numpy(rng.standard_normal(tuple(qkv.shape))).bfloat16()
+        qkv.copy_(x)
+        g.replay()
+        host_table, start, kv, slots, info = op.plan(lens, n, host_table, list(pages), P, T)
+        assert np.array_equal(outs[2].cpu().numpy(), slots) and np.array_equal(table.cpu().numpy(), host_table)
+        op.append(host, x[:, Hq:Hq + H].double().numpy(), x[:, Hq + H:].double().numpy(), slots, 1)
+        assert np.array_equal(cache.cpu().numpy(), host)
+        _close(out, None, op.attention(x[:, :Hq].double().numpy(), host, host_table, start, kv, True), None, host)
+        pages, lens = pages[int(info[1]):], kv.tolist()
+    del g
+
+
 def test_serving_steps_together(dev):
     # plan, append and attend as a server runs them: two prompts in chunks, then decoding, then a third request joins
     H, Hq, d, P, width, n_pages = 2, 8, 128, 16, 12, 40
