@@ -30,6 +30,11 @@ mxattn_status check_cache(const void* cache, int Hkv, int d, int page_size, int6
   return MXATTN_OK;
 }
 
+// The ranges in which rows and units of work are counted.
+bool countable(int R, int Hq, int Hkv, int max_new) {
+  return static_cast<int64_t>(max_new) * (Hq / Hkv) < (1ll << 30) && static_cast<int64_t>(max_new) * Hq < (1ll << 31) / (R > 0 ? R : 1);
+}
+
 // Status area, then the partial rows of split requests.
 size_t paged_workspace(const SplitPlan& s, int d) {
   return 256 + static_cast<size_t>(s.part_rows) * (d + 1) * sizeof(float);
@@ -128,7 +133,9 @@ mxattn_status mxattn_cache_read(const uint8_t* cache, const int64_t* slots, int6
 }
 
 size_t mxattn_paged_workspace_size(int64_t T, int R, int Hq, int Hkv, int d, int max_new, int64_t max_kv) {
-  if (T < 0 || R < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || (d != 64 && d != 128) || max_new < 0 || max_kv < 0) return 0;
+  if (T < 0 || R < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || (d != 64 && d != 128) || max_new < 0 || max_kv < 0 ||
+      !countable(R, Hq, Hkv, max_new))
+    return 0;
   return paged_workspace(plan_splits(R, Hq, Hkv, d, max_new, max_kv), d);
 }
 
@@ -145,8 +152,7 @@ mxattn_status mxattn_paged_forward(const void* q, int64_t q_token_stride, int64_
   if (st != MXATTN_OK) return st;
   if (T >= (1ll << 31)) return MXATTN_ERR_UNSUPPORTED;
   if (!workspace || !aligned(workspace, 256)) return MXATTN_ERR_INVALID_ARG;
-  if (static_cast<int64_t>(max_new) * (Hq / Hkv) >= (1ll << 30) || static_cast<int64_t>(max_new) * Hq >= (1ll << 31) / (R > 0 ? R : 1))
-    return MXATTN_ERR_UNSUPPORTED;
+  if (!countable(R, Hq, Hkv, max_new)) return MXATTN_ERR_UNSUPPORTED;
   const SplitPlan plan = plan_splits(R, Hq, Hkv, d, max_new, max_kv);
   if (plan.units >= (1ll << 31)) return MXATTN_ERR_UNSUPPORTED;
   if (workspace_bytes < paged_workspace(plan, d)) return MXATTN_ERR_WORKSPACE;

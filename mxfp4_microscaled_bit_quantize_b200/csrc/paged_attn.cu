@@ -583,14 +583,16 @@ __global__ void __launch_bounds__(128) paged_combine_kernel(const PagedParams p,
   const int lane = threadIdx.x & 31;
   const int64_t unit = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
   const int64_t per_request = static_cast<int64_t>(p.max_new) * p.Hq;
-  const int r = static_cast<int>(unit / per_request);
-  if (r >= p.R) return;
+  const bool any = unit < p.R * per_request;
+  const int r = any ? static_cast<int>(unit / per_request) : 0;
   const int64_t rest = unit - r * per_request;
   const int i = static_cast<int>(rest / p.Hq), h = static_cast<int>(rest % p.Hq);
   const RequestRange rq = request_range(p, r);
   const int used = static_cast<int>((rq.cap + sp.chunk - 1) / sp.chunk);
-  if (i >= rq.n || used <= 1) return;
-  asm volatile("griddepcontrol.wait;" ::: "memory");      // launched ahead of the parts' end, see launch_rows
+  // Launched ahead of the parts' end, see launch_rows. Every warp waits for it, those with nothing to join too:
+  // the launch behind this one relies on this one's end alone.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!any || i >= rq.n || used <= 1) return;
   const int64_t orow = static_cast<int64_t>(rq.start + i) * p.Hq + h;
   const int64_t prow = ((static_cast<int64_t>(r) * p.max_new + i) * p.Hq + h) * sp.splits;
   const float* lse = sp.part_lse + prow;
@@ -638,6 +640,7 @@ __global__ void __launch_bounds__(128) paged_combine_kernel(const PagedParams p,
 SplitPlan plan_splits(int R, int Hq, int Hkv, int d, int max_new, int64_t max_kv) {
   SplitPlan s{};
   const int64_t rows = static_cast<int64_t>(max_new) * (Hq / Hkv);
+  if (max_kv > 0x7FFFFF00) max_kv = 0x7FFFFF00;              // as in request_range
   s.tc = rows > 16;
   s.nt = rows <= 8 ? 1 : 2;
   const int64_t per = s.tc ? 256 : 8 * s.nt;

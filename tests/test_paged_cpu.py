@@ -76,7 +76,7 @@ PAGED = dict(q=FAKE, qt=512, qh=128, cache=FAKE, table=FAKE, width=4, start=FAKE
     (dict(kv=None), INVALID), (dict(out=None), INVALID), (dict(out=FAKE + 2), INVALID), (dict(lse=FAKE + 2), INVALID), (dict(T=-1), INVALID),
     (dict(T=1 << 31), UNSUPPORTED), (dict(R=-1), INVALID), (dict(Hq=3), INVALID), (dict(Hq=0), INVALID), (dict(H=0), INVALID), (dict(d=96), UNSUPPORTED),
     (dict(page=100), UNSUPPORTED), (dict(pages=-1), INVALID), (dict(new=-1), INVALID), (dict(max_kv=-1), INVALID), (dict(ws=None), INVALID),
-    (dict(ws=FAKE + 64), INVALID), (dict(ws_bytes=0), WORKSPACE), (dict(T=0), OK), (dict(R=0), OK), (dict(new=0), OK)])
+    (dict(ws=FAKE + 64), INVALID), (dict(ws_bytes=0), WORKSPACE), (dict(new=1 << 30), UNSUPPORTED), (dict(R=1 << 20, new=1 << 10), UNSUPPORTED), (dict(T=0), OK), (dict(R=0), OK), (dict(new=0), OK)])
 def test_paged_refusals(lib, change, status):
     a = {**PAGED, **change}
     assert lib.mxattn_paged_forward(a["q"], a["qt"], a["qh"], a["cache"], a["table"], a["width"], a["start"], a["kv"], a["out"], a["lse"], a["T"], a["R"],
@@ -88,8 +88,10 @@ def test_paged_workspace_size(lib):
     # it follows the requests, not the rows of a padded batch
     assert lib.mxattn_paged_workspace_size(1 << 20, 4, 32, 8, 128, 1, 131072) == lib.mxattn_paged_workspace_size(4, 4, 32, 8, 128, 1, 131072) < 64 << 20
     assert lib.mxattn_paged_workspace_size(4096, 1, 32, 8, 128, 4096, 131072) < 256 << 20
+    assert lib.mxattn_paged_workspace_size(4, 4, 32, 8, 128, 1, 1 << 62) < 64 << 20
     for bad in ((-1, 1, 4, 2, 128, 1, 9), (1, -1, 4, 2, 128, 1, 9), (1, 1, 3, 2, 128, 1, 9), (1, 1, 4, 2, 96, 1, 9), (1, 1, 4, 2, 128, -1, 9),
-                (1, 1, 4, 2, 128, 1, -9), (1, 1, 4, 0, 128, 1, 9)):
+                (1, 1, 4, 2, 128, 1, -9), (1, 1, 4, 0, 128, 1, 9), (1, 1, 4, 2, 128, 1 << 30, 9),
+                (1, 1 << 20, 4, 2, 128, 1 << 10, 9)):
         assert lib.mxattn_paged_workspace_size(*bad) == 0
 
 

@@ -404,6 +404,29 @@ def test_paged_two_calls_at_once(dev, n):
         assert all(torch.equal(o, w) for o in outs)
 
 
+@pytest.mark.parametrize("n", [1, 24])
+def test_result_is_there_for_the_next_launch(dev, n):
+    # a bound on the lengths that plans for splits, and lengths that need none: the joining launch has nothing to do
+    # and must not let the stream go on before the parts' launch has ended
+    R, H, Hq, P, L = 16, 2, 8, 64, 6000
+    g = torch.Generator(device=dev).manual_seed(1)
+    pages = R * -(-L // P)
+    cache = torch.randint(0, 256, (pages, H, 2, P * 68), generator=g, device=dev, dtype=torch.uint8)
+    cache[..., P * 64:] = 126
+    cache = cache.view(pages, H, 2, P, 68)
+    table = torch.arange(pages, dtype=torch.int32, device=dev).view(R, -1)
+    q = torch.randn(R * n, Hq, 128, generator=g, device=dev).bfloat16()
+    start, kv = torch.arange(0, R * n + 1, n, dtype=torch.int32, device=dev), torch.full((R,), L, dtype=torch.int32, device=dev)
+    ws = torch.empty(api.paged_workspace_size(R * n, R, Hq, H, 128, n, 1 << 20), dtype=torch.uint8, device=dev)
+    assert ws.numel() > 256
+    for _ in range(20):
+        out = torch.zeros_like(q)
+        api.mxattn_paged_forward(q, cache, table, start, kv, max_new=n, max_kv=1 << 20, workspace=ws, out=out)
+        seen = out.clone()
+        torch.cuda.synchronize()
+        assert torch.equal(seen, out) and bool((out != 0).any())
+
+
 def test_empty_calls(dev):
     cache = api.cache_alloc(3, 2, 64, 16, dev)
     none = torch.empty(0, 2, 64, dtype=torch.bfloat16, device=dev)
