@@ -345,20 +345,21 @@ def test_paged_long_contexts_are_repeatable(dev, lens, Hq, H):
         assert torch.equal(api.mxattn_paged_forward(*on, max_new=n, max_kv=max(host[4]))[:rows], out[:rows])
 
 
-def test_paged_captured_calls_share_a_workspace(dev):
+@pytest.mark.parametrize("n,bound", [(2, 512), (20, 512), (20, 5000)])
+def test_paged_captured_calls_share_a_workspace(dev, n, bound):
     # two graphs over one workspace, replayed in turn for lengths and queries that changed after the capture
-    lens = [(300, 2), (40, 2), (129, 2)]
+    lens = [(302 - n, n), (42 - n, n), (131 - n, n)]
     on, host = make(dev, lens, True, 8, 2, 128, 16, tail=0)
     q, cache, table, start, kv = on
-    ws = torch.empty(api.paged_workspace_size(6, 3, 8, 2, 128, 2, 512), dtype=torch.uint8, device=dev)
+    ws = torch.empty(api.paged_workspace_size(3 * n, 3, 8, 2, 128, n, bound), dtype=torch.uint8, device=dev)
     outs = [torch.zeros_like(q) for _ in range(2)]
     graphs = []
     for i, causal in enumerate((True, False)):
-        api.mxattn_paged_forward(q, cache, table, start, kv, max_new=2, max_kv=512, causal=causal, workspace=ws, out=outs[i])
+        api.mxattn_paged_forward(q, cache, table, start, kv, max_new=n, max_kv=bound, causal=causal, workspace=ws, out=outs[i])
         torch.cuda.synchronize()
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):
-            api.mxattn_paged_forward(q, cache, table, start, kv, max_new=2, max_kv=512, causal=causal, workspace=ws, out=outs[i])
+            api.mxattn_paged_forward(q, cache, table, start, kv, max_new=n, max_kv=bound, causal=causal, workspace=ws, out=outs[i])
         graphs.append(g)
     for kv_now in ([302, 42, 131], [17, 2, 100], [0, 42, 131]):
         kv.copy_(i32(kv_now, dev))
