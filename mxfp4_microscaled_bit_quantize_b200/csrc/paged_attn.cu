@@ -24,9 +24,9 @@
 //     range needs no such care.
 // A long context is split over CTAs (chunk keys each); their results meet in paged_combine_kernel.
 //
-// Measured (d = 128, 32 query and 8 KV heads, pages of 16): 64 requests of up to 8192 keys, one token each, 86 us
-// (267 MB: 3.1 TB/s, 47 % of the copy bandwidth); 2 x 131072 keys, four tokens each, pages of 64: 112 us (285 MB:
-// 2.5 TB/s). The copies alone take 56 us of the 86; the rest is arithmetic that they do not hide: the ALU pipe,
+// Measured (d = 128, 32 query and 8 KV heads, pages of 16): 64 requests of up to 8192 keys, one token each, 89 us
+// (267 MB: 3.0 TB/s, 46 % of the copy bandwidth); 2 x 131072 keys, four tokens each, pages of 64: 114 us (285 MB:
+// 2.5 TB/s). The copies alone take 56 us of the 89; the rest is arithmetic that they do not hide: the ALU pipe,
 // which cvt shares with the logic on nibbles and scale bytes, is 56 % busy, the schedulers issue 64 % of the time
 // with 16 warps of 128 registers. Fragments loaded to registers one group ahead instead of the ring took 94 us, two
 // groups a turn, deeper rings or 12 warps of 168 registers the same as now.
@@ -652,10 +652,23 @@ SplitPlan plan_splits(int R, int Hq, int Hkv, int d, int max_new, int64_t max_kv
   // keys and two column tiles: 115 us, 134 with twice or half as many).
   constexpr int64_t kSpread[3] = {0, 2368, 592};
   int64_t chunk;
-  if (s.tc) chunk = units >= 592 ? max_kv : (units * max_kv + 887) / 888;      // six CTAs for each SM, or four without splits
-  else chunk = (units * max_kv + kSpread[s.nt] - 1) / kSpread[s.nt];
-
-  if (s.tc && chunk < 1024) chunk = 1024;
+  if (s.tc) {
+    // CTAs run one to an SM and a CTA's set-up and output cost about as much as four tiles of 128 keys, so the
+    // splits are chosen by waves x (4 + tiles of a split), joining the parts counted as four more. A split has to
+    // gain a tenth: the bounds overstate ragged batches (7 requests of up to 777 tokens over 3001: 125 us in one
+    // part, 134 in three; 2 x 100 tokens over 8000: 71 us in four parts, 80 in eight; 2048 over 8000: 382 us in
+    // one, 423 in two, 451 in four; 2048 over 30720: 1.19 ms in one, 1.26 in four; 8 over 100000: 134 us in 18
+    // parts, 189 in 98).
+    const int64_t tiles = (max_kv + 127) / 128;
+    int64_t best = 0, parts = 1;
+    for (int64_t n = 1; n <= kMaxSplits && n * 2 <= (tiles > 2 ? tiles : 2) && (n == 1 || units * n <= 1184); ++n) {
+      const int64_t cost = (units * n + 147) / 148 * (4 + (tiles + n - 1) / n) + (n > 1 ? 4 : 0);
+      if (n == 1 || (cost < best && cost * 10 < 9 * (units + 147) / 148 * (4 + tiles))) { best = cost; parts = n; }
+    }
+    chunk = (tiles + parts - 1) / parts * 128;
+  } else {
+    chunk = (units * max_kv + kSpread[s.nt] - 1) / kSpread[s.nt];
+  }
   chunk = (chunk + unit - 1) / unit * unit;
   if (chunk < unit) chunk = unit;
   int64_t splits = (max_kv + chunk - 1) / chunk;

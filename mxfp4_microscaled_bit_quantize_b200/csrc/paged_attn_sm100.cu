@@ -21,9 +21,9 @@
 //                 its reference by 8
 // P is rounded to bf16 (8 bits) for the product, the row sum is taken before the rounding, in fp32.
 //
-// Measured (d = 128): 2048 tokens over 30720 keys, 32 query and 8 KV heads: 1.28 ms, 833 TFLOP/s, 60 % of the
-// bf16 rate sustained under the power limit; 32760 rows x 40 heads over 512 keys: 0.72 ms, 477 TFLOP/s (four key
-// tiles per CTA: set-up, first loads and output are half of its 20 us). A pair of tiles takes about 4300 clocks
+// Measured (d = 128): 2048 tokens over 30720 keys, 32 query and 8 KV heads: 1.19 ms, 894 TFLOP/s, 64 % of the
+// bf16 rate sustained under the power limit; 32760 rows x 40 heads over 512 keys: 0.63 ms, 543 TFLOP/s (four key
+// tiles per CTA: set-up, first loads and output are half of its 18 us). A pair of tiles takes about 4300 clocks
 // per 128 keys: a row tile's own chain (load S and maxima 900, exponentials 1500, hand-over 350, P V 650, S 1050)
 // is what bounds it. Tried and slower: one S buffer for both tiles with P in columns of its own, 64-key steps
 // with two S buffers a tile (M = 128, N = 64 products take as long as N = 128), fp16 tiles with the codes
@@ -447,7 +447,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const PagedPara
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&s.bar_q);
-    // the Q rows of a CTA that will run when this one's place is free, on their way to L2
+    // the Q rows of a CTA that will run when this one's place is free, on their way to L2 (a seventieth of the
+    // time with four key tiles per CTA)
     uint32_t nu = blockIdx.x + kPlaces;
     if (nu < gridDim.x) {
       nu /= sp.splits;
