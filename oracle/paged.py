@@ -102,14 +102,10 @@ def plan(ctx, new, table, free, P, max_tokens):
     return table, np.array(start), np.array(kv), slots, np.array([start[-1], taken, refused, 0])
 
 
-def attention(q, cache, table, q_start, kv_len, causal, max_kv=None):
-    """(out, lse, spread, mass) of the requests' rows: out [T, Hq, d] fp64 and lse [T, Hq], and for tolerances
-    spread = sum_j p_j |v_j| and mass = max_j sum_c |q_c k_jc| / sqrt(d). NaN in rows of no request."""
+def _heads(q, cache, table, q_start, kv_len, causal, max_kv):
+    """(rows, head, q rows, k, v, seen, p before the division, its sums, top) of each request's rows and head."""
     T, Hq, d = q.shape
     n_pages, H, _, P, _ = cache.shape
-    out = np.full((T, Hq, d), np.nan)
-    lse = np.full((T, Hq), np.nan)
-    spread, mass = np.zeros((T, Hq, d)), np.zeros((T, Hq))
     for r in range(len(kv_len)):
         a, n = int(q_start[r]), int(q_start[r + 1] - q_start[r])
         if n <= 0:
@@ -120,20 +116,42 @@ def attention(q, cache, table, q_start, kv_len, causal, max_kv=None):
         there = (page >= 0) & (page < n_pages)
         k, v = read(cache, np.where(there, page * P + pos % P, -1))
         for h in range(Hq):
-            x = q[a:a + n, h] @ k[:, h // (Hq // H)].T / np.sqrt(d)
+            kh, vh, qh = k[:, h // (Hq // H)], v[:, h // (Hq // H)], q[a:a + n, h]
             seen = np.broadcast_to(there, (n, L)).copy()
             if causal:
                 seen &= pos[None] <= (int(kv_len[r]) - n + np.arange(n))[:, None]
-            x = np.where(seen, x, -np.inf)
+            x = np.where(seen, qh @ kh.T / np.sqrt(d), -np.inf)
             top = x.max(axis=1, initial=-np.inf, keepdims=True)
             e = np.where(seen, np.exp(x - np.where(np.isfinite(top), top, 0.0)), 0.0)
-            tot = e.sum(axis=1, keepdims=True)
-            p = np.divide(e, tot, out=np.zeros_like(e), where=tot > 0)
-            vh = v[:, h // (Hq // H)]
-            out[a:a + n, h] = p @ vh
-            spread[a:a + n, h] = p @ np.abs(vh)
-            with np.errstate(divide="ignore"):
-                lse[a:a + n, h] = (np.where(np.isfinite(top), top, 0.0) + np.log(tot))[:, 0]
-            if L:
-                mass[a:a + n, h] = np.where(seen, np.abs(q[a:a + n, h]) @ np.abs(k[:, h // (Hq // H)]).T, 0).max(axis=1) / np.sqrt(d)
+            yield slice(a, a + n), h, qh, kh, vh, seen, e, e.sum(axis=1, keepdims=True), top
+
+
+def attention(q, cache, table, q_start, kv_len, causal, max_kv=None):
+    """(out, lse, spread, mass) of the requests' rows: out [T, Hq, d] fp64 and lse [T, Hq], and for tolerances
+    spread = sum_j p_j |v_j| and mass = max_j sum_c |q_c k_jc| / sqrt(d). NaN in rows of no request."""
+    T, Hq, d = q.shape
+    out = np.full((T, Hq, d), np.nan)
+    lse = np.full((T, Hq), np.nan)
+    spread, mass = np.zeros((T, Hq, d)), np.zeros((T, Hq))
+    for rows, h, qh, kh, vh, seen, e, tot, top in _heads(q, cache, table, q_start, kv_len, causal, max_kv):
+        p = np.divide(e, tot, out=np.zeros_like(e), where=tot > 0)
+        out[rows, h] = p @ vh
+        spread[rows, h] = p @ np.abs(vh)
+        with np.errstate(divide="ignore"):
+            lse[rows, h] = (np.where(np.isfinite(top), top, 0.0) + np.log(tot))[:, 0]
+        if len(kh):
+            mass[rows, h] = np.where(seen, np.abs(qh) @ np.abs(kh).T, 0).max(axis=1) / np.sqrt(d)
     return out, lse, spread, mass
+
+
+def attention_weights(q, cache, table, q_start, kv_len, causal, max_kv=None):
+    """(square, share, apart) [T, Hq, d] for tolerances: square = sum_j p_j^2 v_j^2, share = max_j p_j times the sum of
+    |v_j| over the keys that the row sees, apart = sum_j p_j |v_j - out|."""
+    square, share, apart = np.zeros(q.shape), np.zeros(q.shape), np.zeros(q.shape)
+    for rows, h, _, _, vh, seen, e, tot, _ in _heads(q, cache, table, q_start, kv_len, causal, max_kv):
+        p = np.divide(e, tot, out=np.zeros_like(e), where=tot > 0)
+        square[rows, h] = p ** 2 @ vh ** 2
+        share[rows, h] = p.max(axis=1, initial=0.0, keepdims=True) * (seen.astype(float) @ np.abs(vh))
+        for i, row in zip(range(rows.start, rows.stop), p):
+            apart[i, h] = row @ np.abs(vh - row @ vh)
+    return square, share, apart
