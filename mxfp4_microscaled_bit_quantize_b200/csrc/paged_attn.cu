@@ -191,16 +191,6 @@ __device__ __forceinline__ void v_scale_pairs(const VFrag<2>& f, uint32_t (&s)[2
   }
 }
 
-// Nonzero where a scale byte of the lane's four keys is not within [r - 14, r + 1], r the reference byte of
-// its block (packed in `top` as r + 1). The subtraction borrows only above the first byte that is out of
-// range, which itself shows (for bytes up to r + 240; larger ones are V values past 2^112).
-__device__ __forceinline__ uint32_t v_out_of_range(const VFrag<4>& f, uint32_t top) {
-  return ((top - f.vs.x) | (top - f.vs.y) | (top - f.vs.z) | (top - f.vs.w)) & 0xF0F0F0F0u;
-}
-__device__ __forceinline__ uint32_t v_out_of_range(const VFrag<2>& f, uint32_t top) {
-  return ((top - f.vs.x) | (top - f.vs.y)) & 0xF0F0F0F0u;      // two keys a word: `top` holds the two blocks twice
-}
-
 template <int D, int NT>
 __global__ void __launch_bounds__(kSmallWarps * 32, NT == 1 ? 4 : 2) paged_small_kernel(const PagedParams p, const SplitParams sp) {
   constexpr int NB = D / 32, kRows = 8 * NT, kPad = D + 4;
@@ -317,10 +307,10 @@ __global__ void __launch_bounds__(kSmallWarps * 32, NT == 1 ? 4 : 2) paged_small
 #pragma unroll
     for (int x = 0; x < 2; ++x) { l[nt][x] = 0.f; m[nt][x] = -INFINITY; mu7[nt][x] = 0.f; thr[nt][x] = -INFINITY; }
   }
-  int rb[NB];                                 // reference exponent byte of V's channel blocks
-  uint32_t rb_top = 0u, sc_add[NB];           // the blocks' r + 1 packed; 2^(s - r) as fp16 bits is s 1024 + sc_add
+  int rb[NB];                                 // reference exponent byte r of V's channel blocks, -1 before the first group
+  uint32_t top[NB], sc_add[NB];               // r + 1 in both halves; 2^(s - r) as fp16 bits is s 1024 + sc_add
 #pragma unroll
-  for (int b = 0; b < NB; ++b) { rb[b] = -1; sc_add[b] = 0x04000400u * 16u; }
+  for (int b = 0; b < NB; ++b) { rb[b] = -1; top[b] = 0x7FFF7FFFu; sc_add[b] = 0u; }   // the first group is out of range
 
   auto step = [&](uint32_t slot, int grp, auto&& refill) {
     const int key0 = grp << 4;
@@ -393,9 +383,13 @@ __global__ void __launch_bounds__(kSmallWarps * 32, NT == 1 ? 4 : 2) paged_small
     v_scale_pairs(fv, vs);
     bool wide = false;
     const bool tail = key0 + 16 > lim_max;
-    if (__any_sync(0xffffffffu, v_out_of_range(fv, rb_top) != 0u) || tail) {
+    // In range: s within [r - 14, r + 1]. The subtraction in 16-bit halves of numbers up to 256 is exact: a half that
+    // would borrow is itself negative and shows in its upper bits.
+    uint32_t out_of_range = 0u;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) out_of_range |= (top[b] - vs[b][0]) | (top[b] - vs[b][1]);
+    if (__any_sync(0xffffffffu, (out_of_range & 0xFFF0FFF0u) != 0u) || tail) {
       // a scale above the reference moves it (O is scaled down); one far below takes the wide path
-      rb_top = 0u;
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         if (tail) {                           // tokens behind the end, whatever their bytes say: no scale at all
@@ -425,10 +419,9 @@ __global__ void __launch_bounds__(kSmallWarps * 32, NT == 1 ? 4 : 2) paged_small
           rb[b] = r_new;
         }
         wide |= lo < rb[b] - 14;
-        rb_top |= static_cast<uint32_t>(min(rb[b] + 1, 255)) << (8 * b);
+        top[b] = static_cast<uint32_t>(rb[b] + 1) * 0x00010001u;
         sc_add[b] = static_cast<uint32_t>(15 - rb[b]) * 0x04000400u;
       }
-      if (NB == 2) rb_top |= rb_top << 16;
     }
     // ---- O^T += V^T P^T: P^T (key pairs of column g) by movmatrix. Words w of a key pair hold blocks 2w,
     //      2w + 1; nibbles of the two keys are brought together so that one cvt gives the pair of one channel:
@@ -516,7 +509,8 @@ __global__ void __launch_bounds__(kSmallWarps * 32, NT == 1 ? 4 : 2) paged_small
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   __syncthreads();                            // the rings give way to the results
 
-  // ---- the warps' results meet in shared memory
+  // ---- the warps' results meet in shared memory, each divided by its own row sum before the unit of V's scales comes in:
+  //      p reaches 2^14, so the sums themselves would leave fp32's range for values that fit it
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -530,10 +524,11 @@ __global__ void __launch_bounds__(kSmallWarps * 32, NT == 1 ? 4 : 2) paged_small
         sl[warp][row] = t;
         sm[warp][row] = m[nt][x];
       }
+      const float own = t > 0.f ? 1.f / t : 0.f;
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         const float unit = rb[b] < 0 ? 0.f : pow2_from_byte(static_cast<uint32_t>(rb[b]));
-        const float4 v = make_float4(o[nt][2 * b][x] * unit, o[nt][2 * b][x + 2] * unit, o[nt][2 * b + 1][x] * unit, o[nt][2 * b + 1][x + 2] * unit);
+        const float4 v = make_float4(o[nt][2 * b][x] * own * unit, o[nt][2 * b][x + 2] * own * unit, o[nt][2 * b + 1][x] * own * unit, o[nt][2 * b + 1][x + 2] * own * unit);
         *reinterpret_cast<float4*>(&so[warp][row][32 * b + 4 * g]) = v;
       }
     }
@@ -548,29 +543,33 @@ __global__ void __launch_bounds__(kSmallWarps * 32, NT == 1 ? 4 : 2) paged_small
 #pragma unroll
     for (int w = 0; w < kSmallWarps; ++w) top = fmaxf(top, sm[w][row]);
     const float base = top == -INFINITY ? 0.f : top;
-    float sum = 0.f, acc[kPer];
+    float sum = 0.f, k[kSmallWarps], acc[kPer];
+#pragma unroll
+    for (int w = 0; w < kSmallWarps; ++w) {
+      k[w] = ex2(sm[w][row] - base) * sl[w][row];        // 0 for a warp that saw no key
+      sum += k[w];
+    }
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
 #pragma unroll
     for (int x = 0; x < kPer; ++x) acc[x] = 0.f;
 #pragma unroll
     for (int w = 0; w < kSmallWarps; ++w) {
-      const float k = ex2(sm[w][row] - base);            // 0 for a warp that saw no key
-      sum = fmaf(k, sl[w][row], sum);
+      k[w] *= inv;
 #pragma unroll
-      for (int x = 0; x < kPer; ++x) acc[x] = fmaf(k, so[w][row][lane * kPer + x], acc[x]);
+      for (int x = 0; x < kPer; ++x) acc[x] = fmaf(k[w], so[w][row][lane * kPer + x], acc[x]);
     }
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
     const float lse2 = sum > 0.f ? base - 7.f + log2f(sum) : -INFINITY;
     const int64_t orow = static_cast<int64_t>(rq.start + i) * p.Hq + head * G + h;
     if (used_splits == 1) {
 #pragma unroll
       for (int x = 0; x < kPer; x += 2)
-        *reinterpret_cast<uint32_t*>(p.out + orow * D + lane * kPer + x) = pack_bf162(acc[x] * inv, acc[x + 1] * inv);
+        *reinterpret_cast<uint32_t*>(p.out + orow * D + lane * kPer + x) = pack_bf162(acc[x], acc[x + 1]);
       if (p.lse && lane == 0) p.lse[orow] = lse2 * 0.6931471805599453f;
     } else {
       const int64_t prow = ((static_cast<int64_t>(r) * p.max_new + i) * p.Hq + head * G + h) * sp.splits + split;
       float* po = sp.part_o + prow * D + lane * kPer;
 #pragma unroll
-      for (int x = 0; x < kPer; ++x) po[x] = acc[x] * inv;
+      for (int x = 0; x < kPer; ++x) po[x] = acc[x];
       if (lane == 0) sp.part_lse[prow] = lse2;
     }
   }
@@ -616,6 +615,9 @@ __global__ void __launch_bounds__(128) paged_combine_kernel(const PagedParams p,
   }
 #pragma unroll
   for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) w[j] *= inv;   // before the parts: up to 128 of them times a value could leave fp32's range
 #pragma unroll
   for (int x = 0; x < kPer; ++x) acc[x] = 0.f;
 #pragma unroll
@@ -628,10 +630,9 @@ __global__ void __launch_bounds__(128) paged_combine_kernel(const PagedParams p,
       for (int x = 0; x < kPer; ++x) acc[x] = fmaf(k, po[static_cast<int64_t>(32 * j + s) * D + x], acc[x]);
     }
   }
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
 #pragma unroll
   for (int x = 0; x < kPer; x += 2)
-    *reinterpret_cast<uint32_t*>(p.out + orow * D + lane * kPer + x) = pack_bf162(acc[x] * inv, acc[x + 1] * inv);
+    *reinterpret_cast<uint32_t*>(p.out + orow * D + lane * kPer + x) = pack_bf162(acc[x], acc[x + 1]);
   if (p.lse && lane == 0) p.lse[orow] = sum > 0.f ? (base + log2f(sum)) * 0.6931471805599453f : -INFINITY;
 }
 

@@ -118,3 +118,32 @@ def test_replayed_for_other_lengths(dev, n, bound):
         torch.cuda.synchronize()
         pp.check(out, lse, pp.expected(q.cpu().double().numpy(), host[1], host[2], host[3], now, True))
     del g
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("lens,Hq,H,exp", [
+    ([(31, 1), (36, 1), (0, 1)], 4, 1, 118),                 # whole groups of 16 keys, and a partial one
+    ([(31, 1), (15, 1), (700, 1)], 4, 2, 124),
+    ([(29, 3), (60, 2)], 5, 1, 118),
+    ([(5000, 1), (17, 1)], 8, 2, 118),                       # parts that are joined
+    ([(31, 40), (80, 20)], 4, 2, 116),
+    ([(700, 40)], 4, 2, 108)])
+def test_values_near_the_top_of_the_range(dev, d, lens, Hq, H, exp):
+    # |v| up to 2^(exp + 2): scale bytes of 241 and more from exp = 116 on
+    on, host = make(dev, lens, True, Hq, H, d, 16, seed=exp, scale=lambda rng, k, v: (k, v * 2.0 ** exp))
+    pp.check(*attend(on, lens, True, max(host[4])), pp.expected(*host, True))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("low,high", [(20, 120), (-100, 10), (100, 122)])
+def test_values_of_far_scales_next_to_each_other(dev, d, low, high):
+    # keys of two magnitudes, 2^100 or 2^22 apart, in the same groups of 16 keys and in groups of their own; the row sums
+    # of the large ones alone would hide the small ones, so one request has small ones only behind its first key
+    def scale(rng, k, v):
+        v = v * np.exp2(np.where(rng.random(v.shape[:2] + (1,)) < 0.3, high, low))
+        v[:16] *= 2.0 ** (low - high)
+        return k, np.clip(v, -2.0 ** 122, 2.0 ** 122)
+
+    lens = [(200, 2), (70, 1)]
+    on, host = make(dev, lens, True, 4, 1, d, 32, seed=7, scale=scale)
+    pp.check(*attend(on, lens, True, 202), pp.expected(*host, True))
