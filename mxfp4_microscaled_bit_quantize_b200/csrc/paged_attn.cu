@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(kSmallWarps * 32, NT == 1 ? 4 : 2) paged_small
   constexpr uint32_t kRing = kRingGroups * kGroupBytes<NB>, kRingBytes = kSmallWarps * kRing, kOutBytes = kSmallWarps * kRows * kPad * 4u;
   __shared__ __align__(128) uint8_t ring[kRingBytes > kOutBytes ? kRingBytes : kOutBytes];
   float (*so)[kRows][kPad] = reinterpret_cast<float (*)[kRows][kPad]>(ring);
-  __shared__ float sm[kSmallWarps][kRows], sl[kSmallWarps][kRows];
+  __shared__ float sm[kSmallWarps][kRows], sl[kSmallWarps][kRows], su[kSmallWarps][NB];   // reference, sum of p; unit of a block of V
   const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3u;
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
 
@@ -509,8 +509,11 @@ __global__ void __launch_bounds__(kSmallWarps * 32, NT == 1 ? 4 : 2) paged_small
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   __syncthreads();                            // the rings give way to the results
 
-  // ---- the warps' results meet in shared memory, each divided by its own row sum before the unit of V's scales comes in:
-  //      p reaches 2^14, so the sums themselves would leave fp32's range for values that fit it
+  // ---- the warps' results meet in shared memory. V's references join last, behind the division by the row's sum: p
+  //      reaches 2^14, so the sums themselves in V's units would leave fp32's range for values that fit it.
+#pragma unroll
+  for (int b = 0; b < NB; ++b)
+    if (lane == b) su[warp][b] = rb[b] < 0 ? 0.f : pow2_from_byte(static_cast<uint32_t>(rb[b]));
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -524,11 +527,9 @@ __global__ void __launch_bounds__(kSmallWarps * 32, NT == 1 ? 4 : 2) paged_small
         sl[warp][row] = t;
         sm[warp][row] = m[nt][x];
       }
-      const float own = t > 0.f ? 1.f / t : 0.f;
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        const float unit = rb[b] < 0 ? 0.f : pow2_from_byte(static_cast<uint32_t>(rb[b]));
-        const float4 v = make_float4(o[nt][2 * b][x] * own * unit, o[nt][2 * b][x + 2] * own * unit, o[nt][2 * b + 1][x] * own * unit, o[nt][2 * b + 1][x + 2] * own * unit);
+        const float4 v = make_float4(o[nt][2 * b][x], o[nt][2 * b][x + 2], o[nt][2 * b + 1][x], o[nt][2 * b + 1][x + 2]);
         *reinterpret_cast<float4*>(&so[warp][row][32 * b + 4 * g]) = v;
       }
     }
@@ -546,17 +547,17 @@ __global__ void __launch_bounds__(kSmallWarps * 32, NT == 1 ? 4 : 2) paged_small
     float sum = 0.f, k[kSmallWarps], acc[kPer];
 #pragma unroll
     for (int w = 0; w < kSmallWarps; ++w) {
-      k[w] = ex2(sm[w][row] - base) * sl[w][row];        // 0 for a warp that saw no key
-      sum += k[w];
+      k[w] = ex2(sm[w][row] - base);                     // 0 for a warp that saw no key
+      sum = fmaf(k[w], sl[w][row], sum);
     }
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const float inv = sum > 0.f ? __fdividef(1.f, sum) : 0.f;   // 2^-22; nothing here waits for a division's slow path
 #pragma unroll
     for (int x = 0; x < kPer; ++x) acc[x] = 0.f;
 #pragma unroll
     for (int w = 0; w < kSmallWarps; ++w) {
-      k[w] *= inv;
+      const float unit = su[w][lane * kPer / 32];
 #pragma unroll
-      for (int x = 0; x < kPer; ++x) acc[x] = fmaf(k[w], so[w][row][lane * kPer + x], acc[x]);
+      for (int x = 0; x < kPer; ++x) acc[x] = fmaf(k[w] * inv * so[w][row][lane * kPer + x], unit, acc[x]);
     }
     const float lse2 = sum > 0.f ? base - 7.f + log2f(sum) : -INFINITY;
     const int64_t orow = static_cast<int64_t>(rq.start + i) * p.Hq + head * G + h;
@@ -606,7 +607,7 @@ __global__ void __launch_bounds__(128) paged_combine_kernel(const PagedParams p,
   }
 #pragma unroll
   for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-  const float base = top == -INFINITY ? 0.f : top;
+  const float base = (top == -INFINITY ? 0.f : top) + 7.f;   // weights up to 2^-7: 128 of them times a value stay in fp32's range
   float sum = 0.f, acc[kPer];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -615,9 +616,6 @@ __global__ void __launch_bounds__(128) paged_combine_kernel(const PagedParams p,
   }
 #pragma unroll
   for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) w[j] *= inv;   // before the parts: up to 128 of them times a value could leave fp32's range
 #pragma unroll
   for (int x = 0; x < kPer; ++x) acc[x] = 0.f;
 #pragma unroll
@@ -630,9 +628,10 @@ __global__ void __launch_bounds__(128) paged_combine_kernel(const PagedParams p,
       for (int x = 0; x < kPer; ++x) acc[x] = fmaf(k, po[static_cast<int64_t>(32 * j + s) * D + x], acc[x]);
     }
   }
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
 #pragma unroll
   for (int x = 0; x < kPer; x += 2)
-    *reinterpret_cast<uint32_t*>(p.out + orow * D + lane * kPer + x) = pack_bf162(acc[x], acc[x + 1]);
+    *reinterpret_cast<uint32_t*>(p.out + orow * D + lane * kPer + x) = pack_bf162(acc[x] * inv, acc[x + 1] * inv);
   if (p.lse && lane == 0) p.lse[orow] = sum > 0.f ? (base + log2f(sum)) * 0.6931471805599453f : -INFINITY;
 }
 
