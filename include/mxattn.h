@@ -345,7 +345,8 @@ mxattn_status mxattn_cache_read(const uint8_t* cache, const int64_t* slots, int6
  *   out_i = sum_j softmax_j(q_i . k_j / sqrt(d)) v_j, with the cache's values of k and v. Token i of
  *   n attends to keys j <= kv_len - n + i (causal = 1), or to all j < kv_len (causal = 0: cross
  *   attention to cached states of any other length). Scores and sums are fp32, Q is not quantized,
- *   the probabilities enter their product with 8 significant bits or more.
+ *   the probabilities enter their product with 8 significant bits or more, or with an error of at
+ *   most 2^-25 of the row's largest where that is more.
  *   A row with no key gets out = 0. Rows of no request are left as they were. out must not overlap q.
  *   max_new, max_kv: upper bounds of the requests' new tokens and of kv_len, from which the work is
  *   laid out; rows of a request past max_new are left as they were, keys past max_kv or past

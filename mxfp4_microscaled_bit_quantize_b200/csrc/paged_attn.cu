@@ -20,8 +20,11 @@
 //     lanes is rarely taken; p = 2^(x - m + 7) <= 2^14 is summed in fp32 and rounded to fp16 (11 bits) for the
 //     product;
 //   * V's block scales enter relative to r_b, the largest exponent so far of channel block b, as 2^(s - r_b) in
-//     fp16. A group with a block more than 14 binades below r_b takes a slower path with bf16 operands, whose
-//     range needs no such care.
+//     fp16, where s is at most 6 below r_b: with p's rounding and that of the product, both at steps of 2^-24 when
+//     they are subnormal, a probability is off by half a step of 8 bits or by (1 + 2^6) 2^-32 < 2^-25 of the row's
+//     largest, whichever is more (with 14 instead of 6, 2^-18: small probabilities vanished behind one outlier of V).
+//     A group with a block further below takes a path with bf16 operands, whose 8 bits need no such care (64 requests
+//     of 8192 keys, 32 query and 8 KV heads, d = 128: 156 us, 211 where every group takes it).
 // A long context is split over CTAs (chunk keys each); their results meet in paged_combine_kernel.
 //
 // Measured (d = 128, 32 query and 8 KV heads, pages of 16): 64 requests of up to 8192 keys, one token each, 89 us
@@ -42,6 +45,8 @@ namespace mxattn {
 constexpr int kSmallWarps = 4;
 constexpr int kMaxSplits = 128;
 constexpr int kRingGroups = 4;          // groups of 16 keys in a warp's ring
+constexpr uint32_t kNear = 6;           // V scales this far below their reference stay in fp16; kNear + 1 is a mask of bits
+static_assert(((kNear + 1) & (kNear + 2)) == 0, "differences 0 .. kNear + 1 are told by their upper bits");
 
 template <int NB> struct Frag;          // what a lane holds of 16 keys
 template <> struct Frag<4> { uint4 k0, k1; uint2 ks; };
@@ -308,9 +313,9 @@ __global__ void __launch_bounds__(kSmallWarps * 32, NT == 1 ? 4 : 2) paged_small
     for (int x = 0; x < 2; ++x) { l[nt][x] = 0.f; m[nt][x] = -INFINITY; mu7[nt][x] = 0.f; thr[nt][x] = -INFINITY; }
   }
   int rb[NB];                                 // reference exponent byte r of V's channel blocks, -1 before the first group
-  uint32_t top[NB], sc_add[NB];               // r + 1 in both halves; 2^(s - r) as fp16 bits is s 1024 + sc_add
+  uint32_t top[NB];                           // r + 1 in both halves
 #pragma unroll
-  for (int b = 0; b < NB; ++b) { rb[b] = -1; top[b] = 0x7FFF7FFFu; sc_add[b] = 0u; }   // the first group is out of range
+  for (int b = 0; b < NB; ++b) { rb[b] = -1; top[b] = 0xFFFFFFFFu; }   // the first group is above it
 
   auto step = [&](uint32_t slot, int grp, auto&& refill) {
     const int key0 = grp << 4;
@@ -379,19 +384,26 @@ __global__ void __launch_bounds__(kSmallWarps * 32, NT == 1 ? 4 : 2) paged_small
     VFrag<NB> fv;
     read_v(fv, slot, at);
     refill();
-    uint32_t vs[NB][2];
+    uint32_t vs[NB][2];                       // becomes r + 1 - s in both halves
     v_scale_pairs(fv, vs);
-    bool wide = false;
-    const bool tail = key0 + 16 > lim_max;
-    // In range: s within [r - 14, r + 1]. The subtraction in 16-bit halves of numbers up to 256 is exact: a half that
+    // In range: s within [r - kNear, r + 1]. The subtraction in 16-bit halves of numbers up to 256 is exact: a half that
     // would borrow is itself negative and shows in its upper bits.
     uint32_t out_of_range = 0u;
 #pragma unroll
-    for (int b = 0; b < NB; ++b) out_of_range |= (top[b] - vs[b][0]) | (top[b] - vs[b][1]);
-    if (__any_sync(0xffffffffu, (out_of_range & 0xFFF0FFF0u) != 0u) || tail) {
-      // a scale above the reference moves it (O is scaled down); one far below takes the wide path
+    for (int b = 0; b < NB; ++b) {
+      vs[b][0] = top[b] - vs[b][0];
+      vs[b][1] = top[b] - vs[b][1];
+      out_of_range |= vs[b][0] | vs[b][1];
+    }
+    // One far below takes the wide path; one above the reference, a negative half, moves it (O is scaled down).
+    bool wide = __any_sync(0xffffffffu, (out_of_range & ~((kNear + 1u) * 0x00010001u)) != 0u);
+    const bool tail = key0 + 16 > lim_max;
+    if ((wide && __any_sync(0xffffffffu, (out_of_range & 0x80008000u) != 0u)) || tail) {
+      wide = false;
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
+        vs[b][0] = top[b] - vs[b][0];
+        vs[b][1] = top[b] - vs[b][1];
         if (tail) {                           // tokens behind the end, whatever their bytes say: no scale at all
 #pragma unroll
           for (int h = 0; h < 2; ++h)
@@ -418,9 +430,10 @@ __global__ void __launch_bounds__(kSmallWarps * 32, NT == 1 ? 4 : 2) paged_small
               for (int x = 0; x < 4; ++x) o[nt][2 * b + tt][x] *= down;
           rb[b] = r_new;
         }
-        wide |= lo < rb[b] - 14;
+        wide |= lo < rb[b] - static_cast<int>(kNear);
         top[b] = static_cast<uint32_t>(rb[b] + 1) * 0x00010001u;
-        sc_add[b] = static_cast<uint32_t>(15 - rb[b]) * 0x04000400u;
+        vs[b][0] = top[b] - vs[b][0];
+        vs[b][1] = top[b] - vs[b][1];
       }
     }
     // ---- O^T += V^T P^T: P^T (key pairs of column g) by movmatrix. Words w of a key pair hold blocks 2w,
@@ -447,7 +460,7 @@ __global__ void __launch_bounds__(kSmallWarps * 32, NT == 1 ? 4 : 2) paged_small
 #pragma unroll
         for (int bb = 0; bb < 2; ++bb) {
           const int b = 2 * w + bb;
-          const uint32_t sc0 = vs[b][0] * 1024u + sc_add[b], sc1 = vs[b][1] * 1024u + sc_add[b];   // 2^(s - r)
+          const uint32_t sc0 = 0x40004000u - vs[b][0] * 1024u, sc1 = 0x40004000u - vs[b][1] * 1024u;   // 2^(s - r)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             const uint32_t b0 = hmul2(pt[nt][0], sc0), b1 = hmul2(pt[nt][1], sc1);
@@ -458,35 +471,37 @@ __global__ void __launch_bounds__(kSmallWarps * 32, NT == 1 ? 4 : 2) paged_small
         }
       }
     } else {
-      // bf16 V relative to the reference, code 2^(s - r), exact; P in bf16
+      // bf16: an fp16 code's bits, moved to the places of bf16's exponent and mantissa, are the code times 2^-112, and P
+      // (8 bits) takes 2^(s - r + 112). Exact for s down to r - 112 and p down to 2^-21 of the row's largest.
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         pt[nt][0] = transpose8x8(pack_bf162(pv[nt][0], pv[nt][1]));
         pt[nt][1] = transpose8x8(pack_bf162(pv[nt][2], pv[nt][3]));
       }
+      auto as_bf16 = [](uint32_t h) { return ((h >> 3) & 0x0FFF0FFFu) | (h & 0x80008000u); };
 #pragma unroll
       for (int w = 0; w < NB / 2; ++w) {
         v_pairs(w, ev, od);
 #pragma unroll
         for (int bb = 0; bb < 2; ++bb) {
           const int b = 2 * w + bb;
-          uint32_t e2[2][2], o2[2][2];
+          // exponent fields s - r + 112 + 127 in both halves, 0 (no weight) where that is negative
+          const uint32_t sc0 = (__vmaxu2(0x01F001F0u - vs[b][0], 0x01000100u) - 0x01000100u) << 7;
+          const uint32_t sc1 = (__vmaxu2(0x01F001F0u - vs[b][1], 0x01000100u) - 0x01000100u) << 7;
+          uint32_t a[2][4];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float f0 = exp2f(static_cast<float>(static_cast<int>(vs[b][h] & 0xFFFFu) - rb[b]));
-            const float f1 = exp2f(static_cast<float>(static_cast<int>(vs[b][h] >> 16) - rb[b]));
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-              const float2 aa = __half22float2(*reinterpret_cast<const __half2*>(&ev[h][2 * bb + t]));
-              const float2 zz = __half22float2(*reinterpret_cast<const __half2*>(&od[h][2 * bb + t]));
-              e2[h][t] = pack_bf162(aa.x * f0, aa.y * f1);
-              o2[h][t] = pack_bf162(zz.x * f0, zz.y * f1);
-            }
+          for (int t = 0; t < 2; ++t) {
+            a[t][0] = as_bf16(ev[0][2 * bb + t]);
+            a[t][1] = as_bf16(od[0][2 * bb + t]);
+            a[t][2] = as_bf16(ev[1][2 * bb + t]);
+            a[t][3] = as_bf16(od[1][2 * bb + t]);
           }
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+          for (int nt = 0; nt < NT; ++nt) {
+            const uint32_t b0 = mul_bf162(pt[nt][0], sc0), b1 = mul_bf162(pt[nt][1], sc1);
 #pragma unroll
-            for (int t = 0; t < 2; ++t) mma_bf16(o[nt][2 * b + t], e2[0][t], o2[0][t], e2[1][t], o2[1][t], pt[nt][0], pt[nt][1]);
+            for (int t = 0; t < 2; ++t) mma_bf16(o[nt][2 * b + t], a[t][0], a[t][1], a[t][2], a[t][3], b0, b1);
+          }
         }
       }
     }

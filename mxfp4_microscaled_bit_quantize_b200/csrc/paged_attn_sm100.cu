@@ -121,12 +121,6 @@ __device__ __forceinline__ void drain_wait_tc(uint64_t* bar, uint32_t parity) {
     if (global_timer_ns() - t0 > 200ull * 1000ull * 1000ull) break;
 }
 
-__device__ __forceinline__ uint32_t mul_bf162(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-
 // 16 TMEM lanes, two halves of the warp, the upper one kOff columns on: 16 columns each.
 template <int kOff>
 __device__ __forceinline__ void tmem_ld16x2_16(uint32_t taddr, uint32_t (&r)[16]) {

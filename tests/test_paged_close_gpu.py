@@ -5,6 +5,7 @@ import pytest
 import torch
 
 from mxfp4_microscaled_bit_quantize_b200 import api, build
+from oracle import paged as op
 from tests import paged_parity as pp
 from tests import test_paged_gpu as base
 from tests.test_paged_gpu import SHAPES, i32, make
@@ -147,3 +148,37 @@ def test_values_of_far_scales_next_to_each_other(dev, d, low, high):
     lens = [(200, 2), (70, 1)]
     on, host = make(dev, lens, True, 4, 1, d, 32, seed=7, scale=scale)
     pp.check(*attend(on, lens, True, 202), pp.expected(*host, True))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("group", [1, 12])
+@pytest.mark.parametrize("far", [5, 6, 7, 14, 60])
+def test_small_probabilities_behind_an_outlier_of_v(dev, d, group, far):
+    # One key dominates, a long flat tail of probabilities near 2^-16 adds up to a visible share, and one key without any
+    # weight has values 2^far above all others. Many requests over the same pages, so that a context stays in one part and
+    # a warp meets a quarter of the tail behind the outlier; the first 64 keys give every warp the same beginning.
+    H, P, L, R = 8, 64, 2048, 300
+    rng = np.random.default_rng(far)
+    k, v = np.zeros((2, L, H, d))
+    k[:, :, 1] = rng.choice([0, 0.5, 1, -0.5, -1], (L, H))
+    v[:] = rng.choice([0.5, 1, 1.5, 1.5], (L, H, d))
+    for first in (0, 16, 32, 48):
+        k[first + 1, :, :2] = 3, 0                 # the dominating key, with small values of its own
+        v[first + 1] *= 2.0 ** -3
+        k[first + 2, :, :2] = -6, 0                # no weight
+        v[first + 2] *= 2.0 ** far
+    cache = np.zeros((L // P, H, 2, P, 17 * d // 32), dtype=np.uint8)
+    op.append(cache, k, v, np.arange(L), 1)
+    q = np.zeros((1, H * group, d))
+    q[..., 0], q[..., 1] = (8 if d == 64 else 11.3125) * 3.8125, rng.choice([0.5, 1, 2], (1, H * group))
+    table = np.arange(L // P)[None]
+    q = torch.from_numpy(q).bfloat16()
+    want = pp.expected(q.double().numpy(), cache, table, [0, 1], [L], True)
+    qs = q.to(dev).expand(R, -1, -1)
+    ws = torch.empty(api.paged_workspace_size(R, R, H * group, H, d, 1, L), dtype=torch.uint8, device=dev)
+    assert ws.numel() == 256                       # one part
+    lse = torch.zeros(R, H * group, device=dev)
+    out = api.mxattn_paged_forward(qs, torch.from_numpy(cache).to(dev), i32(np.repeat(table, R, 0), dev), i32(np.arange(R + 1), dev), i32([L] * R, dev), 1,
+                                   max_kv=L, workspace=ws, lse=lse)
+    assert torch.equal(out, out[:1].expand_as(out)) and torch.equal(lse, lse[:1].expand_as(lse))
+    pp.check(out[:1], lse[:1], want)
