@@ -565,7 +565,7 @@ __global__ void __launch_bounds__(kSmallWarps * 32, NT == 1 ? 4 : 2) paged_small
       k[w] = ex2(sm[w][row] - base);                     // 0 for a warp that saw no key
       sum = fmaf(k[w], sl[w][row], sum);
     }
-    const float inv = sum > 0.f ? __fdividef(1.f, sum) : 0.f;   // 2^-22; nothing here waits for a division's slow path
+    const float inv = sum == 0.f ? 0.f : __fdividef(1.f, sum);   // 2^-22; nothing here waits for a division's slow path
 #pragma unroll
     for (int x = 0; x < kPer; ++x) acc[x] = 0.f;
 #pragma unroll
@@ -574,7 +574,7 @@ __global__ void __launch_bounds__(kSmallWarps * 32, NT == 1 ? 4 : 2) paged_small
 #pragma unroll
       for (int x = 0; x < kPer; ++x) acc[x] = fmaf(k[w] * inv * so[w][row][lane * kPer + x], unit, acc[x]);
     }
-    const float lse2 = sum > 0.f ? base - 7.f + log2f(sum) : -INFINITY;
+    const float lse2 = sum == 0.f ? -INFINITY : base - 7.f + log2f(sum);   // NaN stays NaN
     const int64_t orow = static_cast<int64_t>(rq.start + i) * p.Hq + head * G + h;
     if (used_splits == 1) {
 #pragma unroll
@@ -643,11 +643,11 @@ __global__ void __launch_bounds__(128) paged_combine_kernel(const PagedParams p,
       for (int x = 0; x < kPer; ++x) acc[x] = fmaf(k, po[static_cast<int64_t>(32 * j + s) * D + x], acc[x]);
     }
   }
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
   for (int x = 0; x < kPer; x += 2)
     *reinterpret_cast<uint32_t*>(p.out + orow * D + lane * kPer + x) = pack_bf162(acc[x] * inv, acc[x + 1] * inv);
-  if (p.lse && lane == 0) p.lse[orow] = sum > 0.f ? (base + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+  if (p.lse && lane == 0) p.lse[orow] = sum == 0.f ? -INFINITY : (base + log2f(sum)) * 0.6931471805599453f;
 }
 
 // Up to 16 rows (new tokens x heads of a group) go to the mma.sync kernel, whose time does not depend on

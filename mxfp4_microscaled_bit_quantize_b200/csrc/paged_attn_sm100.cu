@@ -555,8 +555,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const PagedPara
       tc_fence_after();
       float sum = l0 + l1;
       sum += __shfl_xor_sync(0xffffffffu, sum, 16);
-      const float inv = sum > 0.f ? 1.f / sum : 0.f;
-      const float lse2 = sum > 0.f ? mu + log2f(sum) : -INFINITY;
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      const float lse2 = sum == 0.f ? -INFINITY : mu + log2f(sum);   // NaN stays NaN
       int64_t orow = static_cast<int64_t>(rq.start + i) * p.Hq + head * G + h;
       const uint32_t live_rows = __popc(__ballot_sync(0xffffffffu, live) & 0xFFFFu);   // the warp's first rows
       // The rows leave through shared memory (Q's, which no product reads any more), so that a store

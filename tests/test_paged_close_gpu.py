@@ -182,3 +182,18 @@ def test_small_probabilities_behind_an_outlier_of_v(dev, d, group, far):
                                    max_kv=L, workspace=ws, lse=lse)
     assert torch.equal(out, out[:1].expand_as(out)) and torch.equal(lse, lse[:1].expand_as(lse))
     pp.check(out[:1], lse[:1], want)
+
+
+@pytest.mark.parametrize("lens", [[(50, 1), (20, 1), (3, 1)], [(40, 3), (9, 2)], [(90, 40), (7, 11)], [(4000, 2), (60, 2)], [(2500, 40), (30, 9)]])
+def test_queries_of_nan_stay_in_their_rows(dev, lens):
+    # out and lse of such a row are NaN (lse = -infinity means that a row has no key); every other row is as usual
+    on, host = make(dev, lens, True, 8, 2, 128, 16, seed=3, tail=0)
+    bad = [0, int(host[3][-1]) - 1]
+    q = host[0].copy()
+    q[bad[0], :, 5], q[bad[1]] = np.nan, np.nan
+    out, lse = attend((torch.from_numpy(q).bfloat16().to(dev), *on[1:]), lens, True, max(host[4]))
+    assert torch.isnan(out[bad]).all() and torch.isnan(lse[bad]).all()
+    want = pp.expected(*host, True)
+    for x in want.values():
+        x[bad] = np.nan
+    pp.check(out, lse, want)
