@@ -309,6 +309,8 @@ size_t mxattn_cache_page_bytes(int Hkv, int page_size, int d);
  * and its kv_len is ctx_len (0 if that is negative). A refused request takes no page, except that
  * once the free pages have run out every later request that needs one is refused too. The rows of
  * refused requests count in q_start, up to max_tokens. One launch; max_tokens < 2^31.
+ * kv_len may be ctx_len itself (lengths advanced in place). No other output may overlap an input or
+ * another output: such a call is refused with MXATTN_ERR_INVALID_ARG.
  */
 mxattn_status mxattn_cache_plan(const int32_t* ctx_len, const int32_t* new_len, int R, int32_t* block_table,
                                 int table_width, const int32_t* free_pages, int n_free, int page_size,

@@ -352,8 +352,9 @@ def mxattn_cache_plan(ctx_len, new_len, block_table, free_pages, page_size: int,
     ctx_len, new_len [R], block_table [R, width] (the pages each request holds; new ones are written in place),
     free_pages [F]: int32 CUDA tensors. Returns (q_start [R + 1] int32, kv_len [R] int32, slots [max_tokens] int64,
     info [4] int32: new tokens, free pages taken, requests refused, 0); `out` takes the same four to be written in
-    place. A request that does not fit (rows past max_tokens, pages past the table or the free list) is refused:
-    its slots are -1, as are those behind the last request."""
+    place (its kv_len may be ctx_len itself; nothing else may overlap). A request that does not fit (rows past
+    max_tokens, pages past the table or the free list) is refused: its slots are -1, as are those behind the last
+    request."""
     _need(block_table, "block_table", torch.int32)
     dev = block_table.get_device()
     if block_table.dim() != 2 or max_tokens < 0:

@@ -144,6 +144,7 @@ struct PlanParams {
   int64_t* slots;           // [max_tokens]
   int64_t max_tokens;
   int32_t* info;            // [4]
+  int in_place;             // kv_len is ctx_len
 };
 cudaError_t launch_plan(const PlanParams& p, cudaStream_t stream);
 

@@ -30,6 +30,12 @@ mxattn_status check_cache(const void* cache, int Hkv, int d, int page_size, int6
   return MXATTN_OK;
 }
 
+struct Span { const void* at; int64_t bytes; };
+bool overlap(const Span& a, const Span& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
+  return a.bytes > 0 && b.bytes > 0 && x < y + static_cast<uintptr_t>(b.bytes) && y < x + static_cast<uintptr_t>(a.bytes);
+}
+
 // The ranges in which rows and units of work are counted.
 bool countable(int R, int Hq, int Hkv, int max_new) {
   return static_cast<int64_t>(max_new) * (Hq / Hkv) < (1ll << 30) && static_cast<int64_t>(max_new) * Hq < (1ll << 31) / (R > 0 ? R : 1);
@@ -62,7 +68,19 @@ mxattn_status mxattn_cache_plan(const int32_t* ctx_len, const int32_t* new_len, 
   if (!aligned(ctx_len, 4) || !aligned(new_len, 4) || !aligned(block_table, 4) || !aligned(free_pages, 4) ||
       !aligned(q_start, 4) || !aligned(kv_len, 4) || !aligned(slots, 8) || !aligned(info, 4))
     return MXATTN_ERR_INVALID_ARG;
+  // Every CTA reads the inputs while others write, so nothing may be both, but for kv_len over ctx_len.
+  const Span ins[] = {{ctx_len, 4ll * R}, {new_len, 4ll * R}, {free_pages, 4ll * n_free}};
+  const Span outs[] = {{kv_len, 4ll * R}, {q_start, 4ll * R + 4}, {slots, 8 * max_tokens}, {info, 16},
+                       {block_table, 4ll * R * table_width}};
+  const bool in_place = R > 0 && kv_len == ctx_len;
+  for (int o = 0; o < 5; ++o) {
+    for (int i = 0; i < 3; ++i)
+      if (!(in_place && o == 0 && i == 0) && overlap(outs[o], ins[i])) return MXATTN_ERR_INVALID_ARG;
+    for (int x = 0; x < o; ++x)
+      if (overlap(outs[o], outs[x])) return MXATTN_ERR_INVALID_ARG;
+  }
   PlanParams p{};
+  p.in_place = in_place ? 1 : 0;
   p.ctx_len = ctx_len;
   p.new_len = new_len;
   p.R = R;
