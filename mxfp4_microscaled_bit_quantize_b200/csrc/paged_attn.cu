@@ -670,15 +670,17 @@ SplitPlan plan_splits(int R, int Hq, int Hkv, int d, int max_new, int64_t max_kv
   if (s.tc) {
     // CTAs run one to an SM and a CTA's set-up and output cost about as much as four tiles of 128 keys, so the
     // splits are chosen by waves x (4 + tiles of a split), joining the parts counted as four more. A split has to
-    // gain a tenth: the bounds overstate ragged batches (7 requests of up to 777 tokens over 3001: 125 us in one
-    // part, 134 in three; 2 x 100 tokens over 8000: 71 us in four parts, 80 in eight; 2048 over 8000: 382 us in
-    // one, 423 in two, 451 in four; 2048 over 30720: 1.19 ms in one, 1.26 in four; 8 over 100000: 134 us in 18
-    // parts, 189 in 98).
+    // gain a tenth: the bounds overstate ragged batches, and parts take workspace (device time; 32 query and 8 KV heads,
+    // d = 128 but for the first: 7 requests of up to 777 tokens over 3001, 15/3 heads, d = 64: 123 us in one part, 132 in
+    // three; 2048 over 8000: 381 us in one, 424 in two, 454 in four; 2048 over 14336: 611, 654, 656; 2048 over 30720: 1204,
+    // 1252, 1187; 800 over 7392: 165, 187, 168; 1024 over 60000: 1126, 1161, 1190, 1120 in eight; 512 over 30000: 577, 312,
+    // 325; 2 x 100 over 8000: 214, 118, 69, 78 in eight; 8 over 100000: 230 in nine, 132 in 18, 187 in 98).
     const int64_t tiles = (max_kv + 127) / 128;
+    const int64_t whole = (units + 147) / 148 * (4 + tiles);
     int64_t best = 0, parts = 1;
     for (int64_t n = 1; n <= kMaxSplits && n * 2 <= (tiles > 2 ? tiles : 2) && (n == 1 || units * n <= 1184); ++n) {
       const int64_t cost = (units * n + 147) / 148 * (4 + (tiles + n - 1) / n) + (n > 1 ? 4 : 0);
-      if (n == 1 || (cost < best && cost * 10 < 9 * (units + 147) / 148 * (4 + tiles))) { best = cost; parts = n; }
+      if (n == 1 || (cost < best && cost * 10 < 9 * whole)) { best = cost; parts = n; }
     }
     chunk = (tiles + parts - 1) / parts * 128;
   } else {
@@ -694,7 +696,7 @@ SplitPlan plan_splits(int R, int Hq, int Hkv, int d, int max_new, int64_t max_kv
   s.chunk = chunk;
   s.splits = splits < 1 ? 1 : splits;
   s.units = units * s.splits;
-  s.part_rows = s.splits > 1 ? static_cast<int64_t>(R) * max_new * Hq * s.splits : 0;   // at most about 890 x 256
+  s.part_rows = s.splits > 1 ? static_cast<int64_t>(R) * max_new * Hq * s.splits : 0;   // at most 1184 x 256
   return s;
 }
 
