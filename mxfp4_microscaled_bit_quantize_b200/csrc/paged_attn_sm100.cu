@@ -17,9 +17,13 @@
 //   warps 4-11    convert: page lookups and code loads one tile ahead in registers, then K(t) and V(t) as bf16
 //                 into a two-stage ring (128-byte swizzle: K is K-major, V MN-major)
 //   warps 12-27   softmax of tiles A and B, two threads per row; the tiles' exponentials take turns, so that one
-//                 tile's products run under the other's; O is rescaled in TMEM only when a row's maximum passes
-//                 its reference by 8
-// P is rounded to bf16 (8 bits) for the product, the row sum is taken before the rounding, in fp32.
+//                 tile's products run under the other's; O is rescaled in TMEM where a row's maximum has grown
+// P is rounded to bf16 (8 bits) for the product: the TMEM operand has V's type, and V needs bf16's range (fp16 tiles with
+// references of their own took 1.40 instead of 1.25 ms); the row sum is taken before the rounding, in fp32. The key that
+// dominates a row enters without a rounding, as P = 1, if the reference follows every larger score. With references that
+// move only past 2^8 it is rounded too, and the error against 64 bits was 1.35e-3 instead of 1.13e-3 (fp32 arithmetic
+// rounded once: 1.12e-3) for 2048 tokens over 30720, 1.05e-3 instead of 0.91e-3 (0.90e-3) for ragged chunks over 3001;
+// following costs 1 to 5 % of the time (1208 -> 1220 us, 123 -> 127 us, 32760 rows over 512 keys 634 -> 670 us).
 //
 // Measured (d = 128): 2048 tokens over 30720 keys, 32 query and 8 KV heads: 1.19 ms, 894 TFLOP/s, 64 % of the
 // bf16 rate sustained under the power limit; 32760 rows x 40 heads over 512 keys: 0.63 ms, 543 TFLOP/s (four key
@@ -45,12 +49,6 @@ constexpr uint32_t kTcCols = 512, kColSx = 0, kColOx = 256;   // S / P of tile X
 constexpr uint32_t kSw128 = 2;                                // descriptor code of the 128-byte swizzle
 constexpr int kTcStages = 2;
 constexpr uint32_t kPlaces = 148;                             // CTAs that run at the same time, one per SM
-// A row's reference moves when a score passes it by this much (in powers of two). bf16 has fp32's range, so a
-// larger step would be safe, but a key that dominates its row enters without a rounding only while it is the
-// reference (P = 1): with 32 the error against 64 bits was 1.7 times that of fp32 arithmetic rounded once,
-// with 8 it is 1.1 to 1.2 times, for 1 % of the time.
-constexpr float kMoveBy = 8.f;
-
 template <int D>
 struct __align__(1024) TcSmem {
   static_assert(D == 64 || D == 128, "Q and the output stage are laid out for these");
@@ -503,7 +501,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const PagedPara
       a2 = fmax3(a2, v[62], v[63]);
       float top = fmaxf(fmax3(a0, a1, a2), a3);
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16)) * c;
-      const bool up = top > m + kMoveBy;
+      const bool up = top > m;
       if (__any_sync(0xffffffffu, up)) {
         const float mn = up ? top : m;
         const float mun = mn == -INFINITY ? 0.f : mn;

@@ -145,13 +145,16 @@ def attention(q, cache, table, q_start, kv_len, causal, max_kv=None):
 
 
 def attention_weights(q, cache, table, q_start, kv_len, causal, max_kv=None):
-    """(square, share, apart) [T, Hq, d] for tolerances: square = sum_j p_j^2 v_j^2, share = max_j p_j times the sum of
-    |v_j| over the keys that the row sees, apart = sum_j p_j |v_j - out|."""
-    square, share, apart = np.zeros(q.shape), np.zeros(q.shape), np.zeros(q.shape)
+    """(square, share, apart, others) [T, Hq, d] for tolerances: square = sum_j p_j^2 v_j^2, share = max_j p_j times the
+    sum of |v_j| over the keys that the row sees, apart = sum_j p_j |v_j - out|, others = square without the largest p_j."""
+    square, share, apart, others = (np.zeros(q.shape) for _ in range(4))
     for rows, h, _, _, vh, seen, e, tot, _ in _heads(q, cache, table, q_start, kv_len, causal, max_kv):
         p = np.divide(e, tot, out=np.zeros_like(e), where=tot > 0)
         square[rows, h] = p ** 2 @ vh ** 2
         share[rows, h] = p.max(axis=1, initial=0.0, keepdims=True) * (seen.astype(float) @ np.abs(vh))
         for i, row in zip(range(rows.start, rows.stop), p):
             apart[i, h] = row @ np.abs(vh - row @ vh)
-    return square, share, apart
+            if len(row):
+                most = np.argmax(row)
+                others[i, h] = np.delete(row, most) ** 2 @ np.delete(vh, most, axis=0) ** 2
+    return square, share, apart, others

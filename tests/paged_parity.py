@@ -25,12 +25,21 @@ from oracle import paged as op
 def expected(q, cache, table, q_start, kv_len, causal, max_kv=None):
     """Everything that `check` compares with, from numpy arrays."""
     out, lse, spread, mass = op.attention(q, cache, table, q_start, kv_len, causal, max_kv)
-    square, share, apart = op.attention_weights(q, cache, table, q_start, kv_len, causal, max_kv)
+    square, share, apart, others = op.attention_weights(q, cache, table, q_start, kv_len, causal, max_kv)
     delta = (q.shape[-1] + 16) * 2.0 ** -24 * mass
     rest = 2.0 ** -18 * spread + 2.0 ** -25 * share + np.expm1(2 * delta)[..., None] * apart
     return {"out": out, "lse": lse, "most": 2.0 ** -8 * (np.abs(out) + spread) + rest,
             "norm": 2 * np.sqrt((2.0 ** -8 * out) ** 2 + 2.0 ** -16 * square) + rest,
-            "lse_most": delta + 2.0 ** -19 + 2.0 ** -22 * np.abs(np.where(np.isfinite(lse), lse, 0))}
+            "others": others, "lse_most": delta + 2.0 ** -19 + 2.0 ** -22 * np.abs(np.where(np.isfinite(lse), lse, 0))}
+
+
+def roundings(want):
+    """The 2-norm that the error of a call's result has if nothing is rounded but out, and each probability but its row's
+    largest to 8 bits: steps of s leave s^2 / 12 each, relative roundings within +-2^-9 leave p^2 2^-18 / 3. Over many
+    rows an error's norm stays within a few hundredths of it."""
+    ref = want["out"][~np.isnan(want["out"][:, 0, 0])]
+    step = np.exp2(np.floor(np.log2(np.maximum(np.abs(ref), 1e-30))) - 7)
+    return np.sqrt(np.sum(step ** 2) / 12 + np.sum(want["others"]) * 2.0 ** -18 / 3)
 
 
 def problems(out, lse, want):

@@ -197,3 +197,17 @@ def test_queries_of_nan_stay_in_their_rows(dev, lens):
     for x in want.values():
         x[bad] = np.nan
     pp.check(out, lse, want)
+
+
+@pytest.mark.parametrize("lens,causal,Hq,H,d", [
+    ([(1500, 100), (700, 90)], True, 8, 2, 128), ([(1400, 130)], True, 6, 6, 64), ([(900, 200)], False, 4, 2, 128),     # many rows a head
+    ([(1500, 2)] * 24, True, 8, 4, 128), ([(1000, 1)] * 48, True, 8, 2, 64)])                                           # few
+def test_dominating_keys_are_not_rounded(dev, lens, causal, Hq, H, d):
+    # peaked rows: what the probability of the largest key costs would show in the norm of the error
+    on, host = make(dev, lens, causal, Hq, H, d, 16, seed=d + Hq, scale=lambda rng, k, v: (3 * k, v))
+    want = pp.expected(*host, causal)
+    out, lse = attend(on, lens, causal, max(host[4]))
+    pp.check(out, lse, want)
+    n = int(host[3][-1])
+    err = np.linalg.norm((out[:n].cpu().double().numpy() - want["out"][:n]).ravel())
+    assert err <= 1.05 * pp.roundings(want), err / pp.roundings(want)
