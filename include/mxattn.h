@@ -354,8 +354,16 @@ mxattn_status mxattn_cache_read(const uint8_t* cache, const int64_t* slots, int6
  *   laid out; rows of a request past max_new are left as they were, keys past max_kv or past
  *   table_width pages are not attended to. Table entries outside [0, n_pages) count as no keys.
  *   q_start values are clamped to [0, T], a negative kv_len counts as 0. Ranges of two requests must
- *   not overlap. Supported: max_new * Hq / Hkv < 2^30, R * max_new * Hq < 2^31.
- *   Two launches at most (the second joins the parts of split contexts), deterministic.
+ *   not overlap. Supported: max_new * Hq / Hkv < 2^30, R * max_new * Hq < 2^31; max_kv counts as
+ *   2^31 - 256 at most.
+ *   Two kernels at most (the second joins the parts of split contexts), where more than 16 rows a
+ *   KV head attend with the clearing of the status word before them; deterministic.
+ *   Ranges: sums are fp32, so |v| times the keys of a request stays below 2^127, and V's blocks of 32
+ *   channels lie within 2^112 of each other between the keys of a request (smaller ones lose bits
+ *   next to larger ones). With up to 16 rows a KV head (max_new * Hq / Hkv), |k| stays below 2^112,
+ *   K blocks of scale 2^-127 count as zero, and elements of q enter the scores with 8 bits or an
+ *   error of 2^-32 of their row's largest or 2^-132, whichever is more. A query with a NaN gives a
+ *   row of NaN, lse included.
  *   workspace: mxattn_paged_workspace_size(...) bytes, 256-byte aligned, contents on entry ignored,
  *   not used concurrently by another call; its first word is the status word of
  *   mxattn_check_status. A call with T, R or max_new 0 does nothing and leaves it as it was.

@@ -28,9 +28,9 @@
 // A long context is split over CTAs (chunk keys each); their results meet in paged_combine_kernel.
 //
 // Measured (d = 128, 32 query and 8 KV heads, pages of 16): 64 requests of up to 8192 keys, one token each, 89 us
-// (267 MB: 3.0 TB/s, 46 % of the copy bandwidth); 2 x 131072 keys, four tokens each, pages of 64: 114 us (285 MB:
-// 2.5 TB/s). The copies alone take 56 us of the 89; the rest is arithmetic that they do not hide: the ALU pipe,
-// which cvt shares with the logic on nibbles and scale bytes, is 56 % busy, the schedulers issue 64 % of the time
+// (267 MB: 3.0 TB/s, 45 % of the copy bandwidth); 2 x 131072 keys, four tokens each, pages of 64: 117 us (285 MB:
+// 2.4 TB/s). The copies alone take 56 us of the 89; the rest is arithmetic that they do not hide: the ALU pipe,
+// which cvt shares with the logic on nibbles and scale bytes, is 58 % busy, the schedulers issue 65 % of the time
 // with 16 warps of 128 registers. Fragments loaded to registers one group ahead instead of the ring took 94 us, two
 // groups a turn, deeper rings or 12 warps of 168 registers the same as now.
 #include <cuda_bf16.h>

@@ -25,9 +25,9 @@
 // rounded once: 1.12e-3) for 2048 tokens over 30720, 1.05e-3 instead of 0.91e-3 (0.90e-3) for ragged chunks over 3001;
 // following costs 1 to 5 % of the time (1208 -> 1220 us, 123 -> 127 us, 32760 rows over 512 keys 634 -> 670 us).
 //
-// Measured (d = 128): 2048 tokens over 30720 keys, 32 query and 8 KV heads: 1.19 ms, 894 TFLOP/s, 64 % of the
-// bf16 rate sustained under the power limit; 32760 rows x 40 heads over 512 keys: 0.63 ms, 543 TFLOP/s (four key
-// tiles per CTA: set-up, first loads and output are half of its 18 us). A pair of tiles takes about 4300 clocks
+// Measured (d = 128): 2048 tokens over 30720 keys, 32 query and 8 KV heads: 1.22 ms, 874 TFLOP/s, 63 % of the
+// bf16 rate sustained under the power limit; 32760 rows x 40 heads over 512 keys: 0.67 ms, 513 TFLOP/s (four key
+// tiles per CTA: set-up, first loads and output are half of its 19 us). A pair of tiles takes about 4300 clocks
 // per 128 keys: a row tile's own chain (load S and maxima 900, exponentials 1500, hand-over 350, P V 650, S 1050)
 // is what bounds it. Tried and slower: one S buffer for both tiles with P in columns of its own, 64-key steps
 // with two S buffers a tile (M = 128, N = 64 products take as long as N = 128), fp16 tiles with the codes

@@ -211,3 +211,14 @@ def test_dominating_keys_are_not_rounded(dev, lens, causal, Hq, H, d):
     n = int(host[3][-1])
     err = np.linalg.norm((out[:n].cpu().double().numpy() - want["out"][:n]).ravel())
     assert err <= 1.05 * pp.roundings(want), err / pp.roundings(want)
+
+
+@pytest.mark.parametrize("n", [1, 3, 40])
+@pytest.mark.parametrize("exp", [-100, -60, 60, 105])
+def test_keys_of_any_range(dev, n, exp):
+    # |k| around 2^exp and queries around 2^-exp: ordinary scores
+    lens = [(300, n), (33, n)]
+    on, host = make(dev, lens, True, 8, 2, 128, 16, seed=n, tail=0, scale=lambda rng, k, v: (k * 2.0 ** exp, v))
+    q = host[0] * 2.0 ** -exp
+    out, lse = attend((torch.from_numpy(q).bfloat16().to(dev), *on[1:]), lens, True, 300 + n)
+    pp.check(out, lse, pp.expected(q, *host[1:], True))
