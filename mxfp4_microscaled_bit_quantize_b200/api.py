@@ -422,7 +422,9 @@ def mxattn_paged_forward(q, cache, block_table, q_start, kv_len, max_new: int, m
     block_table [R, width], q_start [R + 1], kv_len [R] (int32, as mxattn_cache_plan makes them); max_new, max_kv:
     upper bounds of a request's new tokens and of kv_len (default: what the table holds). causal: token i of n sees
     keys up to kv_len - n + i; otherwise all kv_len (cross attention). Returns out [T, Hq, d] bf16; rows of no
-    request are left as they were (whatever they held, in a new `out`). lse: optional fp32 [T, Hq] to be written."""
+    request are left as they were (whatever they held, in a new `out`). lse: optional fp32 [T, Hq] to be written.
+    The kernel is chosen by max_new * Hq / Hkv (up to 16 or more): requests with a long chunk and requests with single
+    tokens are faster in two calls on parts of the same tensors, which leave each other's rows alone."""
     n_pages, Hkv, P, d, dev = _cache(cache)
     T, Hq, qs = _rows(q, "q", None, d, dev)
     _need(block_table, "block_table", torch.int32)

@@ -55,3 +55,39 @@ def test_lengths_advanced_in_place(R, ctx, new, T):
         for a, b, name in zip((got_table, *outs), (table, start, c, slots, info), ("table", "q_start", "kv_len", "slots", "info")):
             assert np.array_equal(a.cpu().numpy(), b), name
         free = free[int(info[1]):]
+
+
+@pytest.mark.gpu
+def test_captured_step_that_advances_lengths_in_place():
+    # one graph, replayed: every replay appends `new` tokens to each request, 8 CTAs in a cluster (more than 512 rows)
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    build.build()
+    dev, P, R = torch.device("cuda:0"), 16, 40
+    rng = np.random.default_rng(1)
+    c, n = rng.integers(0, 50, R), rng.integers(10, 40, R)
+    rows, width = int(n.sum()) + 7, 20
+    assert rows > 512
+    pool = rng.permutation(R * width)
+    held = -(-c // P)
+    table = np.full((R, width), -1)
+    for r in range(R):
+        table[r, :held[r]] = pool[held[:r].sum():held[:r].sum() + held[r]]
+    i32 = lambda x: torch.tensor(np.asarray(x), dtype=torch.int32, device=dev)  # noqa: E731
+    lens, new, got_table, free = i32(c), i32(n), i32(table), i32(np.zeros(R * width))
+    outs = (torch.empty(R + 1, dtype=torch.int32, device=dev), lens, torch.empty(rows, dtype=torch.int64, device=dev),
+            torch.empty(4, dtype=torch.int32, device=dev))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        api.mxattn_cache_plan(lens, new, got_table, free, P, rows, out=outs)
+    left = pool[held.sum():]
+    for _ in range(6):
+        free.zero_()
+        free[:len(left)] = i32(left)
+        g.replay()
+        # the captured call was told of R * width free pages: the ones behind `left` are page 0, which no request reaches
+        table, start, c, slots, info = op.plan(c.tolist(), n.tolist(), table, list(left) + [0] * (R * width - len(left)), P, rows)
+        for a, b, name in zip((got_table, *outs), (table, start, c, slots, info), ("table", "q_start", "kv_len", "slots", "info")):
+            assert np.array_equal(a.cpu().numpy(), b), name
+        left = left[int(info[1]):]
+    del g
