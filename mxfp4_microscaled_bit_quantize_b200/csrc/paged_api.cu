@@ -30,10 +30,10 @@ mxattn_status check_cache(const void* cache, int Hkv, int d, int page_size, int6
   return MXATTN_OK;
 }
 
-struct Span { const void* at; int64_t bytes; };
+struct Span { const void* at; uint64_t bytes; };
 bool overlap(const Span& a, const Span& b) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
-  return a.bytes > 0 && b.bytes > 0 && x < y + static_cast<uintptr_t>(b.bytes) && y < x + static_cast<uintptr_t>(a.bytes);
+  const uint64_t x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
+  return a.bytes > 0 && b.bytes > 0 && (x < y ? y - x < a.bytes : x - y < b.bytes);
 }
 
 // The ranges in which rows and units of work are counted.
@@ -69,9 +69,10 @@ mxattn_status mxattn_cache_plan(const int32_t* ctx_len, const int32_t* new_len, 
       !aligned(q_start, 4) || !aligned(kv_len, 4) || !aligned(slots, 8) || !aligned(info, 4))
     return MXATTN_ERR_INVALID_ARG;
   // Every CTA reads the inputs while others write, so nothing may be both, but for kv_len over ctx_len.
-  const Span ins[] = {{ctx_len, 4ll * R}, {new_len, 4ll * R}, {free_pages, 4ll * n_free}};
-  const Span outs[] = {{kv_len, 4ll * R}, {q_start, 4ll * R + 4}, {slots, 8 * max_tokens}, {info, 16},
-                       {block_table, 4ll * R * table_width}};
+  const uint64_t lens = 4ull * R;
+  const Span ins[] = {{ctx_len, lens}, {new_len, lens}, {free_pages, 4ull * n_free}};
+  const Span outs[] = {{kv_len, lens}, {q_start, lens + 4}, {slots, 8ull * max_tokens}, {info, 16},
+                       {block_table, static_cast<uint64_t>(R) * table_width >= 1ull << 61 ? ~0ull : lens * table_width}};
   const bool in_place = R > 0 && kv_len == ctx_len;
   for (int o = 0; o < 5; ++o) {
     for (int i = 0; i < 3; ++i)

@@ -671,10 +671,10 @@ SplitPlan plan_splits(int R, int Hq, int Hkv, int d, int max_new, int64_t max_kv
     // CTAs run one to an SM and a CTA's set-up and output cost about as much as four tiles of 128 keys, so the
     // splits are chosen by waves x (4 + tiles of a split), joining the parts counted as four more. A split has to
     // gain a tenth: the bounds overstate ragged batches, and parts take workspace (device time; 32 query and 8 KV heads,
-    // d = 128 but for the first: 7 requests of up to 777 tokens over 3001, 15/3 heads, d = 64: 123 us in one part, 132 in
-    // three; 2048 over 8000: 381 us in one, 424 in two, 454 in four; 2048 over 14336: 611, 654, 656; 2048 over 30720: 1204,
-    // 1252, 1187; 800 over 7392: 165, 187, 168; 1024 over 60000: 1126, 1161, 1190, 1120 in eight; 512 over 30000: 577, 312,
-    // 325; 2 x 100 over 8000: 214, 118, 69, 78 in eight; 8 over 100000: 230 in nine, 132 in 18, 187 in 98).
+    // d = 128 but for the first: 7 requests of up to 777 tokens over 3001, 15/3 heads, d = 64: 126 us in one part, 137 in
+    // three; 2048 over 8000: 389 us in one, 441 in two, 477 in four; 2048 over 14336: 622, 673, 684; 2048 over 30720: 1217,
+    // 1275, 1214; 800 over 7392: 171, 194, 177; 1024 over 60000: 1133, 1175, 1215, 1144 in eight; 512 over 30000: 582, 317,
+    // 333; 2 x 100 over 8000: 214, 119, 70, 78 in eight; 8 over 100000: 230 in nine, 131 in 18, 186 in 98).
     const int64_t tiles = (max_kv + 127) / 128;
     const int64_t whole = (units + 147) / 148 * (4 + tiles);
     int64_t best = 0, parts = 1;

@@ -23,7 +23,7 @@
 // dominates a row enters without a rounding, as P = 1, if the reference follows every larger score. With references that
 // move only past 2^8 it is rounded too, and the error against 64 bits was 1.35e-3 instead of 1.13e-3 (fp32 arithmetic
 // rounded once: 1.12e-3) for 2048 tokens over 30720, 1.05e-3 instead of 0.91e-3 (0.90e-3) for ragged chunks over 3001;
-// following costs 1 to 5 % of the time (1208 -> 1220 us, 123 -> 127 us, 32760 rows over 512 keys 634 -> 670 us).
+// following costs 1 to 5 % of the time (1208 -> 1218 us, 123 -> 127 us, 32760 rows over 512 keys 634 -> 670 us).
 //
 // Measured (d = 128): 2048 tokens over 30720 keys, 32 query and 8 KV heads: 1.22 ms, 874 TFLOP/s, 63 % of the
 // bf16 rate sustained under the power limit; 32760 rows x 40 heads over 512 keys: 0.67 ms, 513 TFLOP/s (four key
